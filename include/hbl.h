@@ -326,6 +326,135 @@ hbl_status hbl_fht_ln_backward(const float* g, const void* x, hbl_dtype xt, int6
 hbl_status hbl_kv_quant(const void* x, hbl_dtype xt, int64_t rows, int64_t D, int bits, uint8_t* codes,
                         float* scales, cudaStream_t stream);
 
+/* ---------------------------------------------------------------- a paged 8-bit cache and its attention
+ * Serving form of the low-bit QKV states: keys and values are held as one
+ * unsigned code per byte under hbl_kv_quant's rule, with ONE absmax gamma per
+ * block of tokens and head, and the attention reads the codes.
+ *   codes   device, [num_blocks][H][block][D] bytes (K and V each)
+ *   scales  device, [num_blocks][H] floats: gamma
+ *   a code q stands for (2 q - L) gamma / L, L = 2^bits - 1
+ * A request owns the blocks named by its row of the table, in order: token p
+ * of it lives in block table[b][p / block], at place p % block, and the slot
+ * of a token is its block times `block` plus that place.  block is 16, 32, 64
+ * or 128 tokens, D 32, 64, 128 or 256, bits 2 .. 8, num_blocks * block below
+ * 2^31.  Every index that these calls read from device memory is checked
+ * there: one out of range is passed over, never followed. */
+
+/* The bookkeeping of one step, from lengths alone, in one launch.
+ *   cached       device, [B]: tokens each request has in the cache
+ *   added        device, [B]: token rows it brings in this step (0 allowed)
+ *   B            requests, 1 .. 4096
+ *   free_blocks  device, [num_free]: ids of blocks nobody owns; the step takes
+ *                them in order from place taken[0] on
+ *   table        device, [B][width], updated in place: entries of blocks that
+ *                a request did not have yet are written, no others; blocks
+ *                past `width` are not given out
+ *   T            rows of the step's token batch (it may be longer than the
+ *                sum of `added`), 1 .. 2^26
+ *   total        device, [B] (output): cached + added
+ *   row_start    device, [B + 1] (output): first token row of each request,
+ *                and the end of the last (no entry above T)
+ *   slots        device, [T] (output): slot of each row; -1 for rows behind
+ *                the last request and for tokens without a block
+ *   positions    device, [T] (output): position of each row in its request
+ *                (the caller's RoPE), -1 behind the last request
+ *   taken_out    device, one int (output): taken[0] plus the blocks this step
+ *                needed; above num_free the blocks ran out, and the requests
+ *                that came last got -1 in their table entries
+ * Negative lengths count as 0.  The outputs are buffers of their own: total
+ * is not cached and taken_out not taken, so a call may be repeated. */
+hbl_status hbl_kv_plan(const int32_t* cached, const int32_t* added, int64_t B, int64_t block,
+                       const int32_t* free_blocks, int64_t num_free, const int32_t* taken, int32_t* table,
+                       int64_t width, int64_t T, int32_t* total, int32_t* row_start, int32_t* slots,
+                       int32_t* positions, int32_t* taken_out, cudaStream_t stream);
+
+/* Writes the K and V rows of a step (after RoPE) into the cache.
+ *   k, v      device, T rows of H heads of D values of dtype xt, row t at
+ *             k + t * k_stride elements (columns of a wider matrix are fine:
+ *             strides are multiples of 16 bytes)
+ *   slots     device, [T]: where each row goes; rows with a slot below 0 or
+ *             past the cache are passed over.  Rows of one block stand
+ *             together in rising order, as hbl_kv_plan lays them out, and no
+ *             slot occurs twice
+ * Per (block, head) that gets rows, with m their max|x|: a block whose first
+ * token is among them starts with gamma = m; in a block that holds earlier
+ * tokens gamma' = max(gamma, m), and where that is larger their codes are
+ * requantized from the values they stand for, x = (float)(2 q - L) *
+ * fl(gamma / L).  Codes are hbl_kv_quant's: q = clip(rint(fl(fl(x r) + L/2)),
+ * 0, L), r = L / (2 (gamma' + 1e-5)), every operation rounded once. */
+hbl_status hbl_kv_append(const void* k, const void* v, hbl_dtype xt, int64_t T, int64_t H, int64_t D,
+                         int64_t k_stride, int64_t v_stride, const int32_t* slots, int bits, int64_t num_blocks,
+                         int64_t block, uint8_t* k_codes, float* k_scales, uint8_t* v_codes, float* v_scales,
+                         cudaStream_t stream);
+
+/* Workspace bytes of hbl_kv_attention (0 for sizes it does not support). */
+size_t hbl_kv_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t B);
+
+/* Causal attention of a step's rows over the cache that already holds them.
+ * Row row_start[b] + i of request b (n = row_start[b+1] - row_start[b] rows)
+ * stands at position p = total[b] - n + i and sees tokens 0 .. p:
+ *   o = sum_j softmax_j(scale q . k_j) v_j,   query head h reads head h / (Hq / Hkv)
+ * One row per request is a decode step; many rows are a prompt or a chunk of
+ * one; both may stand in one batch.  A row that sees no token gives 0, rows
+ * outside [row_start[0], row_start[B]) of o are left as they were, and tokens
+ * past the table or in a block outside the cache are not seen.
+ *   q          device, T rows of Hq heads of D values of dtype qt, row t at
+ *              q + t * q_stride elements (a multiple of 16 bytes)
+ *   row_start  device, [B + 1], rising; total device, [B]; B 1 .. 4096
+ *   table      device, [B][width]
+ *   scale_dev  device, one float, or NULL for 1 / sqrt(D)
+ *   o          device, [T][Hq][D] of dtype ot
+ *   workspace  device, 256-byte aligned, >= hbl_kv_attention_workspace_bytes
+ *              bytes; scratch, of one call at a time
+ * Hq a multiple of Hkv, Hq <= 1024.  Scores, softmax sums and outputs are
+ * accumulated in float; codes enter the products exactly; queries (scaled by a
+ * power of two per row) and weights enter them as fp16, in two parts when q is
+ * HBL_F32, so its products carry 22 bits. */
+hbl_status hbl_kv_attention(const void* q, hbl_dtype qt, int64_t T, int64_t q_stride, int64_t Hq, int64_t Hkv,
+                            int64_t D, const int32_t* row_start, const int32_t* total, int64_t B,
+                            const int32_t* table, int64_t width, int64_t num_blocks, int64_t block, int bits,
+                            const uint8_t* k_codes, const float* k_scales, const uint8_t* v_codes,
+                            const float* v_scales, const float* scale_dev, void* o, hbl_dtype ot, void* workspace,
+                            size_t workspace_bytes, cudaStream_t stream);
+
+/* ---------------------------------------------------------------- residual, RMSNorm and quantizer in one pass
+ * The join between two sublayers: the residual stream takes up a sublayer's
+ * output, and the next BitLinear quantizes its norm.  Per row of K values
+ * (K a multiple of 16, 16 .. 32768, not only powers of two):
+ *   h = x + residual                        (rounded to xt)
+ *   t = fl(fl(h * rstd) * gain),  rstd = 1 / sqrt(fl(mean h^2) + 1e-5)
+ *   codes, scales = hbl_fht_quant_i8's quantizer of t (bits 8 absmax, bits 4
+ *                   absmean, one int8 per code: what hbl_gemm_dequant reads)
+ * The mean of h^2 (and of |t| for bits 4) is summed in double and rounded
+ * once, so codes and scales follow from h bit for bit.
+ *   x         device, [M][K] of dtype xt
+ *   residual  device, [M][K] of dtype xt, or NULL for none
+ *   gain      device, K floats, or NULL for 1
+ *   h         device, [M][K] of dtype xt (output; may be x or residual
+ *             itself), or NULL where it is not wanted
+ *   codes     device, int8 [M][K]; scales device, M floats (outputs) */
+hbl_status hbl_add_rms_quant(const void* x, const void* residual, hbl_dtype xt, int64_t M, int64_t K,
+                             const float* gain, int bits, void* h, int8_t* codes, float* scales,
+                             cudaStream_t stream);
+
+/* Workspace bytes of hbl_add_rms_quant_backward (0 for unsupported sizes). */
+size_t hbl_add_rms_quant_backward_workspace_bytes(int64_t M, int64_t K);
+
+/* Its gradient, straight through the quantizer: from g_t (of t) and g_h (what
+ * reaches h along the residual stream), with n = h rstd,
+ *   g_x = g_h + rstd (g_t gain - n mean(g_t gain n))     (of x and of residual alike)
+ *   g_gain = sum over rows of g_t n
+ *   h      device, [M][K] of dtype xt, as hbl_add_rms_quant wrote it
+ *   g_t    device, [M][K] of dtype gt; g_h device, [M][K] of dtype xt, or NULL
+ *   gain   device, K floats, or NULL for 1
+ *   g_x    device, [M][K] of dtype xt (output; may be g_h itself)
+ *   g_gain device, K floats (output), or NULL where it is not wanted
+ * Sums over a row are float, those over the rows float in fixed order.
+ * workspace device, 256-byte aligned. */
+hbl_status hbl_add_rms_quant_backward(const void* h, hbl_dtype xt, int64_t M, int64_t K, const float* gain,
+                                      const void* g_t, hbl_dtype gt, const void* g_h, void* g_x, float* g_gain,
+                                      void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
 /* ---------------------------------------------------------------- test hooks */
 
 /* Stages 1-2 alone: t = H LN(x) / sqrt(K) as float [M][K] (device output).

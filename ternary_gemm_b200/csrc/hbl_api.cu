@@ -3,6 +3,7 @@
 #include <cstdint>
 
 #include "common.cuh"
+#include "serving.cuh"
 
 namespace {
 
@@ -95,6 +96,45 @@ BackwardLayout backward_layout(int64_t M, int64_t K, int64_t N) {
   L.gt_off = L.q16_off + align256(m * k * 2);
   L.total = L.gt_off + align256(m * k * 4);
   return L;
+}
+
+// ---- the paged cache
+
+bool block_ok(int64_t block) { return block == 16 || block == 32 || block == 64 || block == 128; }
+
+hbl_status check_head_dim(int64_t D) {
+  if (D <= 0) return HBL_ERR_INVALID_ARG;
+  return D == 32 || D == 64 || D == 128 || D == 256 ? HBL_OK : HBL_ERR_UNSUPPORTED;
+}
+
+// num_blocks blocks of `block` tokens: slots are 32-bit
+hbl_status check_cache(int64_t num_blocks, int64_t block, int bits) {
+  if (num_blocks <= 0 || block <= 0 || bits <= 0) return HBL_ERR_INVALID_ARG;
+  if (!block_ok(block) || bits < 2 || bits > 8 || num_blocks > INT32_MAX / block) return HBL_ERR_UNSUPPORTED;
+  return HBL_OK;
+}
+
+hbl_status check_requests(int64_t B, int64_t width) {
+  if (B <= 0 || width <= 0) return HBL_ERR_INVALID_ARG;
+  return B > hbl::kMaxRequests || width > INT32_MAX ? HBL_ERR_UNSUPPORTED : HBL_OK;
+}
+
+// rows of `heads` heads of D values, `stride` elements apart, 16-byte steps
+hbl_status check_row_stride(int64_t stride, int64_t heads, int64_t D, hbl_dtype t) {
+  if (stride < heads * D || stride % (t == HBL_BF16 ? 8 : 4) != 0) return HBL_ERR_INVALID_ARG;
+  return stride > (int64_t(1) << 32) ? HBL_ERR_UNSUPPORTED : HBL_OK;
+}
+
+hbl_status check_heads(int64_t Hq, int64_t Hkv) {
+  if (Hq <= 0 || Hkv <= 0) return HBL_ERR_INVALID_ARG;
+  return Hq > 1024 || Hq % Hkv != 0 ? HBL_ERR_UNSUPPORTED : HBL_OK;
+}
+
+// ---- rows of the residual + RMSNorm kernels
+
+hbl_status check_rms_k(int64_t K) {
+  if (K <= 0) return HBL_ERR_INVALID_ARG;
+  return K % 16 != 0 || K > 32768 ? HBL_ERR_UNSUPPORTED : HBL_OK;
 }
 
 }  // namespace
@@ -459,6 +499,118 @@ hbl_status hbl_kv_quant(const void* x, hbl_dtype xt, int64_t rows, int64_t D, in
   if ((D != 32 && D != 64 && D != 128 && D != 256) || bits < 2 || bits > 8 || rows > kMaxRows * 64)
     return HBL_ERR_UNSUPPORTED;
   return cuda_status(hbl::launch_kv_quant(x, xt == HBL_BF16, rows, D, bits, codes, scales, stream));
+}
+
+hbl_status hbl_kv_plan(const int32_t* cached, const int32_t* added, int64_t B, int64_t block,
+                       const int32_t* free_blocks, int64_t num_free, const int32_t* taken, int32_t* table,
+                       int64_t width, int64_t T, int32_t* total, int32_t* row_start, int32_t* slots,
+                       int32_t* positions, int32_t* taken_out, cudaStream_t stream) {
+  if (!cached || !added || !free_blocks || !taken || !table || !total || !row_start || !slots || !positions ||
+      !taken_out || num_free < 0)
+    return HBL_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)cached, (const void*)added, (const void*)free_blocks, (const void*)taken,
+                        (const void*)table, (const void*)total, (const void*)row_start, (const void*)slots,
+                        (const void*)positions, (const void*)taken_out})
+    if (!aligned(p, 4)) return HBL_ERR_INVALID_ARG;
+  if (total == cached || total == added || taken_out == taken) return HBL_ERR_INVALID_ARG;
+  if (block <= 0) return HBL_ERR_INVALID_ARG;
+  if (!block_ok(block)) return HBL_ERR_UNSUPPORTED;
+  hbl_status s = check_requests(B, width);
+  if (s != HBL_OK) return s;
+  if ((s = check_rows(T)) != HBL_OK) return s;
+  const hbl::KvPlanArgs a = {cached, added, (int)B,    (int)block, free_blocks, num_free,  taken,    table,
+                             width,  T,     total,     row_start,  slots,       positions, taken_out};
+  return cuda_status(hbl::launch_kv_plan(a, stream));
+}
+
+hbl_status hbl_kv_append(const void* k, const void* v, hbl_dtype xt, int64_t T, int64_t H, int64_t D,
+                         int64_t k_stride, int64_t v_stride, const int32_t* slots, int bits, int64_t num_blocks,
+                         int64_t block, uint8_t* k_codes, float* k_scales, uint8_t* v_codes, float* v_scales,
+                         cudaStream_t stream) {
+  if (!k || !v || !slots || !k_codes || !k_scales || !v_codes || !v_scales || !dtype_ok(xt)) return HBL_ERR_INVALID_ARG;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 4) || !aligned(k_codes, 16) || !aligned(v_codes, 16) ||
+      !aligned(k_scales, 4) || !aligned(v_scales, 4) || k_codes == v_codes || k_scales == v_scales)
+    return HBL_ERR_INVALID_ARG;
+  hbl_status s = check_heads(H, H);
+  if (s != HBL_OK) return s;
+  if ((s = check_head_dim(D)) != HBL_OK) return s;
+  if ((s = check_rows(T)) != HBL_OK) return s;
+  if ((s = check_cache(num_blocks, block, bits)) != HBL_OK) return s;
+  if ((s = check_row_stride(k_stride, H, D, xt)) != HBL_OK) return s;
+  if ((s = check_row_stride(v_stride, H, D, xt)) != HBL_OK) return s;
+  const hbl::KvAppendArgs a = {k,     v,    xt == HBL_BF16, T,          (int)H,  (int)D,   k_stride, v_stride,
+                               slots, bits, num_blocks,     (int)block, k_codes, k_scales, v_codes,  v_scales};
+  return cuda_status(hbl::launch_kv_append(a, stream));
+}
+
+size_t hbl_kv_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t B) {
+  if (check_rows(T) != HBL_OK || check_heads(Hq, Hkv) != HBL_OK || check_head_dim(D) != HBL_OK ||
+      check_requests(B, 1) != HBL_OK)
+    return 0;
+  return hbl::kv_attention_workspace(T, (int)Hq, (int)Hkv, (int)D, (int)B);
+}
+
+hbl_status hbl_kv_attention(const void* q, hbl_dtype qt, int64_t T, int64_t q_stride, int64_t Hq, int64_t Hkv,
+                            int64_t D, const int32_t* row_start, const int32_t* total, int64_t B,
+                            const int32_t* table, int64_t width, int64_t num_blocks, int64_t block, int bits,
+                            const uint8_t* k_codes, const float* k_scales, const uint8_t* v_codes,
+                            const float* v_scales, const float* scale_dev, void* o, hbl_dtype ot, void* workspace,
+                            size_t workspace_bytes, cudaStream_t stream) {
+  if (!q || !row_start || !total || !table || !k_codes || !k_scales || !v_codes || !v_scales || !o || !dtype_ok(qt) ||
+      !dtype_ok(ot))
+    return HBL_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(o, 16) || !aligned(k_codes, 16) || !aligned(v_codes, 16) || !aligned(k_scales, 4) ||
+      !aligned(v_scales, 4) || !aligned(row_start, 4) || !aligned(total, 4) || !aligned(table, 4) ||
+      (scale_dev && !aligned(scale_dev, 4)) || o == q)
+    return HBL_ERR_INVALID_ARG;
+  hbl_status s = check_heads(Hq, Hkv);
+  if (s != HBL_OK) return s;
+  if ((s = check_head_dim(D)) != HBL_OK) return s;
+  if ((s = check_rows(T)) != HBL_OK) return s;
+  if ((s = check_requests(B, width)) != HBL_OK) return s;
+  if ((s = check_cache(num_blocks, block, bits)) != HBL_OK) return s;
+  if ((s = check_row_stride(q_stride, Hq, D, qt)) != HBL_OK) return s;
+  if (!workspace || !aligned(workspace, 256) ||
+      workspace_bytes < hbl_kv_attention_workspace_bytes(T, Hq, Hkv, D, B))
+    return HBL_ERR_WORKSPACE;
+  const hbl::KvAttentionArgs a = {q,       qt == HBL_BF16, T,        q_stride,   (int)Hq,   (int)Hkv, (int)D, row_start,
+                                  total,   (int)B,         table,    width,      num_blocks, (int)block, bits, k_codes,
+                                  k_scales, v_codes,       v_scales, scale_dev,  o,         ot == HBL_BF16, workspace};
+  return cuda_status(hbl::launch_kv_attention(a, stream));
+}
+
+hbl_status hbl_add_rms_quant(const void* x, const void* residual, hbl_dtype xt, int64_t M, int64_t K,
+                             const float* gain, int bits, void* h, int8_t* codes, float* scales,
+                             cudaStream_t stream) {
+  if (!x || !codes || !scales || !dtype_ok(xt) || (bits != 4 && bits != 8)) return HBL_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(gain, 16) || !aligned(h, 16) || !aligned(codes, 16) ||
+      !aligned(scales, 4))
+    return HBL_ERR_INVALID_ARG;
+  hbl_status s = check_rms_k(K);
+  if (s != HBL_OK) return s;
+  if ((s = check_rows(M)) != HBL_OK) return s;
+  return cuda_status(hbl::launch_add_rms_quant(x, residual, xt == HBL_BF16, M, K, gain, bits, h, codes, scales, stream));
+}
+
+size_t hbl_add_rms_quant_backward_workspace_bytes(int64_t M, int64_t K) {
+  if (check_rms_k(K) != HBL_OK || check_rows(M) != HBL_OK) return 0;
+  return hbl::add_rms_backward_workspace(M, K);
+}
+
+hbl_status hbl_add_rms_quant_backward(const void* h, hbl_dtype xt, int64_t M, int64_t K, const float* gain,
+                                      const void* g_t, hbl_dtype gt, const void* g_h, void* g_x, float* g_gain,
+                                      void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  if (!h || !g_t || !g_x || !dtype_ok(xt) || !dtype_ok(gt)) return HBL_ERR_INVALID_ARG;
+  if (!aligned(h, 16) || !aligned(gain, 16) || !aligned(g_t, 16) || !aligned(g_h, 16) || !aligned(g_x, 16) ||
+      !aligned(g_gain, 16) || g_x == h || g_x == g_t)
+    return HBL_ERR_INVALID_ARG;
+  hbl_status s = check_rms_k(K);
+  if (s != HBL_OK) return s;
+  if ((s = check_rows(M)) != HBL_OK) return s;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < hbl_add_rms_quant_backward_workspace_bytes(M, K))
+    return HBL_ERR_WORKSPACE;
+  return cuda_status(hbl::launch_add_rms_quant_backward(h, xt == HBL_BF16, M, K, gain, g_t, gt == HBL_BF16, g_h, g_x,
+                                                        g_gain, workspace, stream));
 }
 
 hbl_status hbl_last_device_error(cudaStream_t stream) {
