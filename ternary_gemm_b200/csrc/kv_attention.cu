@@ -15,8 +15,8 @@
 // row into fp16 (bf16 values exactly; float ones as two fp16 parts, 22 bits,
 // and the weights too).
 //
-// One step takes sixteen tokens, which always lie in one block, against eight
-// or sixteen rows (query heads of one cached head, times the request's rows).
+// One step takes thirty-two tokens (each sixteen of them lie in one block)
+// against eight or sixteen rows (query heads of one cached head, times the request's rows).
 // Both products have the codes as their 16-row operand and the rows as the
 // 8-column one, S^T = K Q^T and O^T = V^T W^T, so that the few rows of a decode
 // step cost no empty half of a product.  Such a step is bound by the codes'
@@ -27,7 +27,9 @@
 // whole writes o; parts go to the workspace as (max, sum, o) and a second
 // kernel joins them in order.
 #include <cstdint>
+#include <utility>
 
+#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -42,20 +44,21 @@ using sm100::smem_u32;
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kJoinThreads = 256;
-constexpr int kTok = 16;        // tokens of a tile
+constexpr int kTok = 16;        // tokens that surely lie in one block
+constexpr int kStep = 2 * kTok; // tokens of a tile: two products' depth
 constexpr float kTop = 15.0f;   // log2 of the largest weight in the second product
 constexpr float kLog2e = 1.4426950408889634f;
 // a warp takes at least this many tiles of the line
-constexpr int kMinTiles = 4;
+constexpr int kMinTiles = 2;
 
-// Blocks per SM and stages per warp: copies in flight (over 100 KB on an SM)
+// Blocks per SM and stages per warp: copies in flight (about 100 KB on an SM)
 // and warps enough to hide the products' latency, at the registers that the
 // accumulators (4 NT D / 16 per thread) and the queries leave.
 __host__ __device__ constexpr int blocks_per_sm(int D, int NT, bool f32) {
   const int weight = D * NT * (f32 ? 3 : 2);   // registers go with accumulators and query parts
-  return weight <= 256 ? 4 : (weight <= 384 ? 3 : (weight <= 768 ? 2 : 1));
+  return weight <= 128 ? 4 : (weight <= 384 ? 3 : (weight <= 768 && D < 256 ? 2 : 1));
 }
-__host__ __device__ constexpr int stages_of(int D) { return D >= 128 ? 3 : 6; }
+__host__ __device__ constexpr int stages_of(int D) { return D >= 128 ? 2 : (D == 64 ? 3 : 6); }
 
 // Rows, tiles per row tile, and row tiles of a request.
 struct Request {
@@ -63,7 +66,7 @@ struct Request {
   int n;            // rows
   int keys;         // tokens that the table can hold of it
   int pos0;         // position of its first row (negative where it has fewer tokens than rows)
-  int tiles;        // 16-token tiles of one item
+  int tiles;        // 32-token tiles of one item
   int64_t items;    // row tiles x cached heads
 };
 
@@ -76,7 +79,7 @@ __device__ __forceinline__ Request request_of(const KvAttentionArgs& a, int b, i
   const int64_t limit = a.width * a.block;
   r.pos0 = total - r.n;
   r.keys = limit < total ? (int)limit : total;
-  r.tiles = max((int)(((int64_t)r.keys + kTok - 1) / kTok), 1);  // a request without tokens still writes its zeros
+  r.tiles = max((int)(((int64_t)r.keys + kStep - 1) / kStep), 1);  // a request without tokens still writes its zeros
   r.items = ((int64_t)r.n * (a.Hq / a.Hkv) + rows_per_tile - 1) / rows_per_tile * a.Hkv;
   return r;
 }
@@ -162,8 +165,9 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   return d;
 }
 
+template <int kOff>
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  asm volatile("cp.async.cg.shared.global [%0+%2], [%1+%2], 16;" ::"r"(dst), "l"(src), "n"(kOff) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -171,22 +175,38 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+template <int kOff>
 __device__ __forceinline__ void ldmatrix4t(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4+%5];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
+               : "r"(addr), "n"(kOff)
                : "memory");
 }
 
+template <int kOff>
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4+%5];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr), "n"(kOff)
+               : "memory");
   return v;
 }
+template <int kOff>
 __device__ __forceinline__ uint2 lds64(uint32_t addr) {
   uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2+%3];" : "=r"(v.x), "=r"(v.y) : "r"(addr), "n"(kOff) : "memory");
   return v;
+}
+
+// f(0), f(1), ... f(N - 1) with the argument a constant
+template <int... I, typename F>
+__device__ __forceinline__ void unrolled(std::integer_sequence<int, I...>, F&& f) {
+  (f(std::integral_constant<int, I>()), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void unrolled(F&& f) {
+  unrolled(std::make_integer_sequence<int, N>(), static_cast<F&&>(f));
 }
 
 // over the eight lanes that hold one row's tokens
@@ -203,19 +223,27 @@ __device__ __forceinline__ float row_sum(float v) {
 
 template <bool BF16, int N>
 __device__ __forceinline__ void store_row(void* o, int64_t at, const float (&v)[N]) {
-  if (BF16) {
-    uint32_t w[N / 2];
-#pragma unroll
-    for (int i = 0; i < N / 2; ++i)
-      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(v[2 * i + 1]), "f"(v[2 * i]));
-    if constexpr (N == 4)
-      *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(o) + at) = make_uint2(w[0], w[N / 2 - 1]);
+  if constexpr (N == 1) {
+    if (BF16)
+      reinterpret_cast<__nv_bfloat16*>(o)[at] = __float2bfloat16_rn(v[0]);
     else
-      *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(o) + at) = w[0];
-  } else if constexpr (N == 4) {
-    *reinterpret_cast<float4*>(reinterpret_cast<float*>(o) + at) = make_float4(v[0], v[1], v[N - 2], v[N - 1]);
+      reinterpret_cast<float*>(o)[at] = v[0];
   } else {
-    *reinterpret_cast<float2*>(reinterpret_cast<float*>(o) + at) = make_float2(v[0], v[1]);
+    uint32_t w[N];
+#pragma unroll
+    for (int i = 0; i < N / (BF16 ? 2 : 1); ++i) {
+      if (BF16)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(v[(2 * i + 1) % N]), "f"(v[2 * i % N]));
+      else
+        w[i] = __float_as_uint(v[i]);
+    }
+    char* to = reinterpret_cast<char*>(o) + at * (BF16 ? 2 : 4);
+    if constexpr (N * (BF16 ? 2 : 4) == 4)
+      *reinterpret_cast<uint32_t*>(to) = w[0];
+    else if constexpr (N * (BF16 ? 2 : 4) == 8)
+      *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
+    else
+      *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2 % N], w[3 % N]);
   }
 }
 
@@ -327,10 +355,13 @@ __device__ __forceinline__ void load_query(const KvAttentionArgs& a, const Reque
 // What a warp leaves in the workspace: (max, sum, o) of a part of an item (in
 // slot 2 w the part that it begins in the middle of an item, in slot 2 w + 1
 // the one that it leaves unfinished), and a record of the item that it began
-// and did not end.
+// and did not end.  A CTA whose whole share lies in one item joins its warps'
+// parts itself and leaves one, in its first warp's name.
 struct Record {
-  int64_t i0, i1, per;  // the item's tiles in the line, and a warp's share
-  int b, row0, h, open; // open: there is such an item
+  int64_t mid_cta, last_cta;  // the parts: `head` warps from this one on, `mid` CTAs from mid_cta on, `tail` warps
+  int head, mid, tail;        // from the first of last_cta on; none at all: no open item
+  int row, rows, h;           // first of the item's rows (in the request), their number, cached head
+  int row0;                   // the request's first row of the batch
 };
 struct Parts {
   float* o;        // [slots][rows][D]
@@ -349,13 +380,14 @@ __host__ __device__ inline Parts parts_of(void* workspace, int64_t workers, int 
 template <int D, int NT, bool F32>
 __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, NT, F32)) kv_attention_kernel(const KvAttentionArgs a) {
   constexpr int kStages = stages_of(D);
-  constexpr int kHalf = kTok * D;           // bytes of one of K and V in a stage
-  constexpr int kStage = 2 * kHalf;
+  constexpr int kHalf = kTok * D;           // bytes of sixteen tokens of K or V
+  constexpr int kStage = 4 * kHalf;         // K and V of a tile: K, V of the first sixteen tokens, K, V of the others
   constexpr int kSegs = D / 16;
   constexpr int kRows = 8 * NT;
   constexpr int kCopies = kHalf >= 512 ? kHalf / 512 : 1;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t warp_sums[kWarps];
+  __shared__ float2 cta_ml[kWarps][kRows];
   int64_t* start = reinterpret_cast<int64_t*>(smem + kWarps * kStages * kStage);
 
   // programmatic dependent of the stream's previous kernel: nothing is read before it has ended, and the joining
@@ -377,7 +409,19 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, NT, F32)) kv_attent
   const uint32_t minus = 0xE400E400u | ((uint32_t)(1 << (a.bits - 1)) * 0x10001u);  // -(1024 + z), twice
   const float scale = a.scale ? *a.scale : rsqrtf((float)D);
   const int g = a.Hq / a.Hkv;
-  if (u >= u_end && lane == 0) parts.record[worker].open = 0;
+  // the CTA's share, and whether one item holds it
+  const int64_t c0 = (int64_t)blockIdx.x * kWarps * per, c1 = min(c0 + kWarps * per, units);
+  bool alone = false;
+  if (c0 < c1) {
+    const int b = find_request(start, a.B, c0);
+    const int tiles = request_of(a, b, kRows).tiles;
+    const int64_t end = start[b] + ((c0 - start[b]) / tiles + 1) * tiles;
+    alone = c1 <= end;
+  }
+  if ((u >= u_end || (alone && warp != 0)) && lane == 0) {
+    Record& rec = parts.record[worker];
+    rec.head = rec.mid = rec.tail = 0;
+  }
 
   // where this lane's copies land and its reads begin within a stage
   const uint32_t k_to = k_place<D>(lane / (D / 16), lane % (D / 16));
@@ -397,12 +441,11 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, NT, F32)) kv_attent
     const int64_t i0 = u - t0;
     u += t1 - t0;
 
-    Query<D, NT, F32> q;
-    load_query<D, NT, F32>(a, r, row0, h, lane, scale, q);
     // tokens that the tile's first and last row see, and tiles to work on (none: n <= 0)
     const int all_see = min(r.pos0 + row0 / g + 1, r.keys);
     const int any_sees = min(r.pos0 + (min(row0 + kRows, r.n * g) - 1) / g + 1, r.keys);
-    const int n = min(t1, any_sees > 0 ? (any_sees - 1) / kTok + 1 : 0) - t0;
+    const int n = min(t1, any_sees > 0 ? (any_sees - 1) / kStep + 1 : 0) - t0;
+    const int first = t0 * 2, seen = any_sees > 0 ? (any_sees - 1) / kTok + 1 - first : 0;  // the same in sixteens
 
     float o[NT][kSegs][4];
     float m[NT][2], l[NT][2], w_sum[NT][2];
@@ -416,41 +459,46 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, NT, F32)) kv_attent
       for (int x = 0; x < 2; ++x) m[nt][x] = -INFINITY, l[nt][x] = 0.0f, w_sum[nt][x] = 0.0f;
     }
 
-    // blocks and scales of 32 tiles at a time, one per lane, a group ahead
+    // blocks and scales of 32 sixteens of tokens at a time, one per lane, a group ahead
     const int32_t* pages = a.table + (int64_t)b * a.width;
-    int id_now, id_next;
-    float ku_now, vu_now, ku_next, vu_next;
-    auto look_up = [&](int first, int& id, float& ku, float& vu) {
-      id = -1;
-      ku = 0.0f;
-      vu = 1.0f;
-      if (first + lane < n) {
-        const int v = pages[((t0 + first + lane) * kTok) >> block_shift];
-        if (v >= 0 && v < a.num_blocks) {
-          id = v;
-          const int64_t tile = (int64_t)v * a.Hkv + h;
-          ku = __fdiv_rn(a.k_scales[tile], (float)L);
-          vu = __fdiv_rn(a.v_scales[tile], (float)L);
-        }
+    // (id; scale of the keys; log2 of the values' scale; 0, 1 for values that are all zero, 2 for an absent block)
+    int id_now, id_next, kind_now, kind_next;
+    float ku_now, lu_now, ku_next, lu_next;
+    auto page_of = [&](int i) {
+      const int v = i + lane < seen ? pages[((first + i + lane) * kTok) >> block_shift] : -1;
+      return v >= 0 && v < a.num_blocks ? v : -1;
+    };
+    auto scales_of = [&](int id, float& ku, float& lu, int& kind) {
+      ku = lu = 0.0f;
+      kind = 2;
+      if (id >= 0) {
+        const int64_t tile = (int64_t)id * a.Hkv + h;
+        const float k = a.k_scales[tile], v = a.v_scales[tile];
+        ku = __fdiv_rn(k, (float)L);
+        const float vu = __fdiv_rn(v, (float)L);
+        kind = vu >= 1e-30f ? 0 : 1;
+        lu = __log2f(fmaxf(vu, 1e-30f));
       }
     };
-    look_up(0, id_now, ku_now, vu_now);
-    look_up(32, id_next, ku_next, vu_next);
+    id_now = page_of(0);
+    id_next = page_of(32);
 
     uint32_t into = 0;      // the stage that the next copies fill
     auto issue = [&](int i, int id_of_group) {
-      const int id = __shfl_sync(0xffffffffu, id_of_group, i & 31);
-      if (i < n && id >= 0) {
-        const int64_t from = (((int64_t)id * a.Hkv + h) * a.block + (((t0 + i) * kTok) & (a.block - 1))) * D + lane * 16;
-        const uint8_t *k_src = a.k_codes + from, *v_src = a.v_codes + from;
-        const uint32_t to = ring + into;
-        if (kHalf >= 512 || lane < kHalf / 16) {
 #pragma unroll
-          for (int x = 0; x < kCopies; ++x) {
-            cp_async16(to + k_to + x * 512, k_src + x * 512);
-            // 32 pieces on, the token's part of the place changes by a constant
-            cp_async16(to + kHalf + (v_to ^ (v_place<D>(x * 32 / (D / 16), 0) & 112)) + x * 512, v_src + x * 512);
-          }
+      for (int half = 0; half < 2; ++half) {
+        const int id = __shfl_sync(0xffffffffu, id_of_group, (2 * i + half) & 31);
+        if (i < n && id >= 0) {
+          const int64_t from =
+              (((int64_t)id * a.Hkv + h) * a.block + (((first + 2 * i + half) * kTok) & (a.block - 1))) * D + lane * 16;
+          const uint8_t *k_src = a.k_codes + from, *v_src = a.v_codes + from;
+          const uint32_t to = ring + into + half * 2 * kHalf;
+          if (kHalf >= 512 || lane < kHalf / 16)
+            unrolled<kCopies>([&](auto x) {
+              cp_async16<x * 512>(to + k_to, k_src);
+              // 32 pieces on, the token's part of the place changes by a constant
+              cp_async16<x * 512>(to + kHalf + (v_to ^ (v_place<D>(x * 32 / (D / 16), 0) & 112)), v_src);
+            });
         }
       }
       cp_commit();
@@ -458,107 +506,130 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, NT, F32)) kv_attent
     };
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) issue(i, id_now);
+    scales_of(id_now, ku_now, lu_now, kind_now);
+    scales_of(id_next, ku_next, lu_next, kind_next);
+    Query<D, NT, F32> q;
+    load_query<D, NT, F32>(a, r, row0, h, lane, scale, q);
 
     uint32_t stage = ring;
     for (int i = 0; i < n; ++i) {
-      if (i != 0 && (i & 31) == 0) {
+      if (i != 0 && (i & 15) == 0) {
         id_now = id_next;
         ku_now = ku_next;
-        vu_now = vu_next;
-        look_up(i + 32, id_next, ku_next, vu_next);
+        lu_now = lu_next;
+        kind_now = kind_next;
+        id_next = page_of(2 * i + 32);
+        scales_of(id_next, ku_next, lu_next, kind_next);
       }
       cp_wait<kStages - 2>();
       __syncwarp();  // tile i has landed for all lanes, and all have read the stage that the next copies overwrite
-      issue(i + kStages - 1, (i & 31) + kStages - 1 < 32 ? id_now : id_next);
+      issue(i + kStages - 1, (i & 15) + kStages - 1 < 16 ? id_now : id_next);
 
-      float s[NT][4];
+      float s[2][NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int half = 0; half < 2; ++half) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x) s[nt][x] = 0.0f;
-      if constexpr (D >= 64) {
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int j = 0; j < D / 64; ++j) {
-          // D >= 128: the halves of odd tokens stand the other way round
-          const uint32_t at = D >= 128 ? stage + ((k_from ^ (64 * (j & 1))) + 128 * (j >> 1)) : stage + k_from;
-          const uint4 x0 = lds128(at), x1 = lds128(at + 8 * D);
-          const uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w}, w1[4] = {x1.x, x1.y, x1.z, x1.w};
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const uint32_t k[4] = {codes2(w0[x], 0x4140u, minus), codes2(w1[x], 0x4140u, minus),
-                                   codes2(w0[x], 0x4342u, minus), codes2(w1[x], 0x4342u, minus)};
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma(s[nt], k, q.hi[nt][4 * j + x]);
-              if constexpr (F32) mma(s[nt], k, q.lo[nt][4 * j + x]);
-            }
-          }
-        }
-      } else {
-        const uint2 x0 = lds64(stage + k_from), x1 = lds64(stage + k_from + 8 * D);
-        const uint32_t w0[2] = {x0.x, x0.y}, w1[2] = {x1.x, x1.y};
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const uint32_t k[4] = {codes2(w0[x], 0x4140u, minus), codes2(w1[x], 0x4140u, minus),
-                                 codes2(w0[x], 0x4342u, minus), codes2(w1[x], 0x4342u, minus)};
+          for (int x = 0; x < 4; ++x) s[half][nt][x] = 0.0f;
+      }
+      unrolled<2>([&](auto half) {
+        constexpr int kAt = half * 2 * kHalf;
+        auto steps = [&](int step, uint32_t w0, uint32_t w1) {
+          const uint32_t k[4] = {codes2(w0, 0x4140u, minus), codes2(w1, 0x4140u, minus), codes2(w0, 0x4342u, minus),
+                                 codes2(w1, 0x4342u, minus)};
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            mma(s[nt], k, q.hi[nt][x]);
-            if constexpr (F32) mma(s[nt], k, q.lo[nt][x]);
+            mma(s[half][nt], k, q.hi[nt][step]);
+            if constexpr (F32) mma(s[half][nt], k, q.lo[nt][step]);
           }
+        };
+        if constexpr (D >= 64) {
+          unrolled<D / 64>([&](auto j) {
+            // D >= 128: the halves of odd tokens stand the other way round
+            const uint32_t at = D >= 128 ? stage + (k_from ^ (64 * (j & 1))) : stage + k_from;
+            const uint4 x0 = lds128<kAt + (j >> 1) * 128>(at), x1 = lds128<kAt + (j >> 1) * 128 + 8 * D>(at);
+            steps(4 * j, x0.x, x1.x);
+            steps(4 * j + 1, x0.y, x1.y);
+            steps(4 * j + 2, x0.z, x1.z);
+            steps(4 * j + 3, x0.w, x1.w);
+          });
+        } else {
+          const uint2 x0 = lds64<kAt>(stage + k_from), x1 = lds64<kAt + 8 * D>(stage + k_from);
+          steps(0, x0.x, x1.x);
+          steps(1, x0.y, x1.y);
         }
-      }
+      });
 
-      const bool here = __shfl_sync(0xffffffffu, id_now, i & 31) >= 0;
-      const float ku = __shfl_sync(0xffffffffu, ku_now, i & 31), vu = __shfl_sync(0xffffffffu, vu_now, i & 31);
-      // a block whose values are all zero (below 1e-30) takes part in the sum alone
-      const bool zero = !(vu >= 1e-30f);
-      const float lu = __log2f(zero ? 1e-30f : vu), inv_vu = ex2(-lu);
-      const int tok0 = (t0 + i) * kTok;
-      const bool masked = !here || tok0 + kTok > all_see;
+      int kind[2];
+      float ku[2], lu[2], inv_vu[2];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int from = (2 * i + half) & 31;
+        kind[half] = __shfl_sync(0xffffffffu, kind_now, from);
+        ku[half] = __shfl_sync(0xffffffffu, ku_now, from);
+        lu[half] = __shfl_sync(0xffffffffu, lu_now, from);
+        inv_vu[half] = ex2(-lu[half]);
+      }
+      const int tok0 = (first + 2 * i) * kTok;
+      const bool masked = kind[0] == 2 || kind[1] == 2 || tok0 + kStep > all_see;
       float grow[NT][2];
       bool grows = false;
-      uint32_t w_hi[NT][2], w_lo[F32 ? NT : 1][2];
+      uint32_t w_hi[2][NT][2], w_lo[2][F32 ? NT : 1][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        // s[0], s[1]: token lane / 4, rows 2 c and 2 c + 1; s[2], s[3]: token lane / 4 + 8
-        float p[2][2];
+        // s[.][.][0], [1]: token lane / 4, rows 2 c and 2 c + 1; [2], [3]: token lane / 4 + 8.  p: its log2 weight
+        float p[2][2][2];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const float f1 = q.scale[nt][x] * ku, f0 = q.sum[nt][x] * f1, f = 2.0f * f1;
-          p[0][x] = fmaf(s[nt][x], f, f0);
-          p[1][x] = fmaf(s[nt][2 + x], f, f0);
-        }
-        if (masked) {
+        for (int half = 0; half < 2; ++half)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const int sees = min(r.pos0 + (row0 + nt * 8 + 2 * c + x) / g + 1, r.keys) - tok0;
-            if (!here || gid >= sees) p[0][x] = -INFINITY;
-            if (!here || gid + 8 >= sees) p[1][x] = -INFINITY;
+            const float f = q.scale[nt][x] * ku[half], f0 = fmaf(q.sum[nt][x], f, lu[half]), f2 = 2.0f * f;
+            p[half][0][x] = fmaf(s[half][nt][x], f2, f0);
+            p[half][1][x] = fmaf(s[half][nt][2 + x], f2, f0);
           }
+        if (masked) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const int sees = min(r.pos0 + (row0 + nt * 8 + 2 * c + x) / g + 1, r.keys) - tok0 - half * kTok;
+              if (kind[half] == 2 || gid >= sees) p[half][0][x] = -INFINITY;
+              if (kind[half] == 2 || gid + 8 >= sees) p[half][1][x] = -INFINITY;
+            }
         }
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const float top = fmaxf(m[nt][x], row_max(fmaxf(p[0][x], p[1][x])) + lu);
+          const float top = fmaxf(
+              m[nt][x], row_max(fmaxf(fmaxf(p[0][0][x], p[0][1][x]), fmaxf(p[1][0][x], p[1][1][x]))));
           // a row that has seen nothing keeps -inf, with 0 in its place in the differences
-          const float base = top == -INFINITY ? 0.0f : top, off = lu + kTop - base;
+          const float base = top == -INFINITY ? 0.0f : top, off = kTop - base;
           grow[nt][x] = ex2(m[nt][x] - base);
           grows |= grow[nt][x] != 1.0f;
           m[nt][x] = top;
-          p[0][x] = ex2(p[0][x] + off);
-          p[1][x] = ex2(p[1][x] + off);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            p[half][0][x] = ex2(p[half][0][x] + off);
+            p[half][1][x] = ex2(p[half][1][x] + off);
+          }
         }
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const uint32_t hi = zero ? 0u : pack2(p[y][0], p[y][1]);
-          w_hi[nt][y] = transpose8(hi);
-          if constexpr (F32) w_lo[nt][y] = transpose8(zero ? 0u : pack2(p[y][0] - half_lo(hi), p[y][1] - half_hi(hi)));
+        for (int half = 0; half < 2; ++half) {
+          // a block whose values are all zero (below 1e-30) takes part in the sum alone
+          const bool zero = kind[half] == 1;
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const uint32_t hi = zero ? 0u : pack2(p[half][y][0], p[half][y][1]);
+            w_hi[half][nt][y] = transpose8(hi);
+            if constexpr (F32)
+              w_lo[half][nt][y] = transpose8(zero ? 0u : pack2(p[half][y][0] - half_lo(hi), p[half][y][1] - half_hi(hi)));
+          }
         }
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const float sum = p[0][x] + p[1][x];
-          w_sum[nt][x] = fmaf(w_sum[nt][x], grow[nt][x], zero ? 0.0f : sum);
-          l[nt][x] = fmaf(l[nt][x], grow[nt][x], sum * inv_vu);
+          const float s0 = p[0][0][x] + p[0][1][x], s1 = p[1][0][x] + p[1][1][x];
+          w_sum[nt][x] = fmaf(w_sum[nt][x], grow[nt][x], (kind[0] == 1 ? 0.0f : s0) + (kind[1] == 1 ? 0.0f : s1));
+          l[nt][x] = fmaf(l[nt][x], grow[nt][x], fmaf(s0, inv_vu[0], s1 * inv_vu[1]));
         }
       }
       if (__any_sync(0xffffffffu, grows)) {
@@ -569,30 +640,35 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, NT, F32)) kv_attent
 #pragma unroll
             for (int y = 0; y < 4; ++y) o[nt][x][y] *= grow[nt][y & 1];
       }
-#pragma unroll
-      for (int x = 0; x < kSegs; x += 2) {
+      unrolled<kSegs / 2>([&](auto pair) {
         // four 8 x 16-byte matrices: tokens 0-7 and 8-15 at two neighbouring 16-byte columns; a register holds two
         // tokens at two columns, the even column of a pair in rows 0-7 of the product and the odd one in rows 8-15
-        uint32_t w[4];
-        ldmatrix4t(stage + (D >= 128 ? (v_from ^ (16 * (x & 6))) + 128 * (x >> 3) : v_from ^ (16 * x)), w);
+        constexpr int x = 2 * pair;
+        const uint32_t at = stage + (v_from ^ (16 * (x & 6)));
+        unrolled<2>([&](auto half) {
+          uint32_t w[4];
+          ldmatrix4t<half * 2 * kHalf + (x >> 3) * 128>(at, w);
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const uint32_t v[4] = {codes2(w[2 * y], 0x4240u, minus), codes2(w[2 * y], 0x4341u, minus),
-                                 codes2(w[2 * y + 1], 0x4240u, minus), codes2(w[2 * y + 1], 0x4341u, minus)};
+          for (int y = 0; y < 2; ++y) {
+            const uint32_t v[4] = {codes2(w[2 * y], 0x4240u, minus), codes2(w[2 * y], 0x4341u, minus),
+                                   codes2(w[2 * y + 1], 0x4240u, minus), codes2(w[2 * y + 1], 0x4341u, minus)};
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma(o[nt][x + y], v, w_hi[nt]);
-            if constexpr (F32) mma(o[nt][x + y], v, w_lo[nt]);
+            for (int nt = 0; nt < NT; ++nt) {
+              mma(o[nt][x + y], v, w_hi[half][nt]);
+              if constexpr (F32) mma(o[nt][x + y], v, w_lo[half][nt]);
+            }
           }
-        }
-      }
+        });
+      });
       stage = stage == ring + (kStages - 1) * kStage ? ring : stage + kStage;
     }
     cp_wait<0>();
     __syncwarp();  // the ring is free for the next item
 
-    const bool whole = t0 == 0 && t1 == r.tiles;
+    const bool whole = t0 == 0 && t1 == r.tiles && !alone;
     const int64_t slot = worker * 2 + (t0 == 0 ? 1 : 0);
+    // parts go to the workspace, or to this warp's own stages for the CTA to join
+    float* part = alone ? reinterpret_cast<float*>(smem + warp * kStages * kStage) : parts.o + slot * kRows * D;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -612,123 +688,178 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, NT, F32)) kv_attent
             else
               store_row<false>(a.o, at + 16 * s + 2 * gid, v);
           } else {
-            store_row<false>(parts.o, (slot * kRows + in_tile) * D + 16 * s + 2 * gid, v);
+            store_row<false>(part, in_tile * D + 16 * s + 2 * gid, v);
           }
         }
-        if (!whole && gid == 0) parts.ml[slot * kRows + in_tile] = make_float2(m[nt][x], sum);
+        if (!whole && gid == 0) {
+          if (alone)
+            cta_ml[warp][in_tile] = make_float2(m[nt][x], sum);
+          else
+            parts.ml[slot * kRows + in_tile] = make_float2(m[nt][x], sum);
+        }
       }
-    if (u >= u_end && lane == 0) {
+    if (alone) {
+      // every warp of the CTA that has a share comes here once
+      const int shares = (int)((c1 - c0 + per - 1) / per);
+      asm volatile("bar.sync 1, %0;" ::"r"(shares * 32) : "memory");
+      const bool all = i0 >= c0 && i0 + r.tiles <= c1;
+      const int64_t to = ((int64_t)blockIdx.x * kWarps * 2 + (i0 >= c0 ? 1 : 0)) * kRows;
+      for (int y = warp; y < kRows && row0 + y < r.n * g; y += shares) {
+        float top = -INFINITY, sum = 0.0f;
+        for (int w = 0; w < shares; ++w) top = fmaxf(top, cta_ml[w][y].x);
+        const float base = top == -INFINITY ? 0.0f : top;
+        float v[D / 32];
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) v[i] = 0.0f;
+        for (int w = 0; w < shares; ++w) {
+          const float f = ex2(cta_ml[w][y].x - base);
+          sum = fmaf(f, cta_ml[w][y].y, sum);
+          const float* from = reinterpret_cast<const float*>(smem + w * kStages * kStage) + y * D;
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) v[i] = fmaf(f, from[i * 32 + lane], v[i]);
+        }
+        const int row = row0 + y;
+        const int64_t at = ((int64_t)(r.row0 + row / g) * a.Hq + (int64_t)h * g + row % g) * D;
+        const float inv = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          if (!all)
+            parts.o[(to + y) * D + i * 32 + lane] = v[i];
+          else if (a.o_bf16)
+            reinterpret_cast<__nv_bfloat16*>(a.o)[at + i * 32 + lane] = __float2bfloat16_rn(v[i] * inv);
+          else
+            reinterpret_cast<float*>(a.o)[at + i * 32 + lane] = v[i] * inv;
+        }
+        if (!all && lane == 0) parts.ml[to + y] = make_float2(top, sum);
+      }
+    }
+    if (u >= u_end && lane == 0 && (!alone || warp == 0)) {
       Record rec;
-      rec.i0 = i0;
-      rec.i1 = i0 + r.tiles;
-      rec.per = per;
-      rec.b = b;
-      rec.row0 = row0;
-      rec.h = h;
-      rec.open = t0 == 0 && t1 < r.tiles;
+      rec.head = rec.mid = rec.tail = 0;
+      if (alone ? i0 >= c0 && i0 + r.tiles > c1 : t0 == 0 && t1 < r.tiles) {
+        // an item begun here and left open; CTAs that lie in it whole left one part each
+        const int64_t i1 = i0 + r.tiles, w1 = (i1 - 1) / per, share = kWarps * per;
+        const int64_t first_cta = blockIdx.x;
+        rec.last_cta = w1 / kWarps;
+        const bool last_in = rec.last_cta * share >= i0 && min((rec.last_cta + 1) * share, units) <= i1;
+        rec.head = alone ? 0 : (int)(min(w1, first_cta * kWarps + kWarps - 1) - worker + 1);
+        rec.mid_cta = alone ? first_cta : first_cta + 1;
+        rec.mid = (int)max((last_in ? rec.last_cta : rec.last_cta - 1) - rec.mid_cta + 1, (int64_t)0);
+        rec.tail = last_in || rec.last_cta == first_cta ? 0 : (int)(w1 - rec.last_cta * kWarps + 1);
+        rec.row = row0;
+        rec.rows = min(kRows, r.n * g - row0);
+        rec.h = h;
+        rec.row0 = r.row0;
+      }
       parts.record[worker] = rec;
     }
   }
 }
 
-// Joins the parts of an item that more than one warp worked on: CTA w the item
-// that warp w began and left open.  A warp takes a row and every n-th part.
+// Joins the parts of the items that more than one warp worked on: CTA i those
+// that the warps of CTA i began and left open, a warp per row.
 template <int D, int NT>
 __global__ void __launch_bounds__(kJoinThreads) kv_attention_join_kernel(const KvAttentionArgs a) {
   constexpr int kRows = 8 * NT;
-  constexpr int kJoinWarps = kJoinThreads / 32;
-  constexpr int V = D / 32;
-  __shared__ float part_o[kJoinWarps][D];
-  __shared__ float2 part_ml[kJoinWarps];
+  constexpr int V = D >= 128 ? 4 : D / 32;       // neighbouring values per lane
+  constexpr int kCols = D / (32 * V);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // the parts are the previous kernel's; every CTA waits, so that the end of this grid is the end of that one too
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t workers = gridDim.x, w0 = blockIdx.x;
-  const Parts parts = parts_of(a.workspace, workers, D, kRows);
-  const Record rec = parts.record[w0];
-  if (!rec.open) return;
-  const Request r = request_of(a, rec.b, kRows);
-  const int count = (int)((rec.i1 - 1) / rec.per - w0 + 1);
+  const Parts parts = parts_of(a.workspace, (int64_t)gridDim.x * kWarps, D, kRows);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = a.Hq / a.Hkv;
-  const int rows = min(kRows, r.n * g - rec.row0);
-  const int sharing = rows >= kJoinWarps ? 1 : kJoinWarps / rows;   // warps per row
-  for (int y0 = 0; y0 < rows; y0 += kJoinWarps / sharing) {
-    const int y = y0 + warp / sharing, first = warp % sharing;
-    const bool on = y < rows && warp < kJoinWarps / sharing * sharing;
-    float acc[V], top = -INFINITY, sum = 0.0f;
+  int dealt = 0;  // rows dealt out to the warps so far
+  for (int own = 0; own < kWarps; ++own) {
+    const int64_t w0 = (int64_t)blockIdx.x * kWarps + own;
+    const Record rec = parts.record[w0];
+    const int count = rec.head + rec.mid + rec.tail;
+    if (count == 0) continue;
+    for (int y = (warp - dealt) & (kJoinThreads / 32 - 1); y < rec.rows; y += kJoinThreads / 32) {
+      auto slot = [&](int p) {
+        const int64_t w = p < rec.head ? w0 + p
+                                       : (p < rec.head + rec.mid ? (rec.mid_cta + p - rec.head) * kWarps
+                                                                 : rec.last_cta * kWarps + p - rec.head - rec.mid);
+        return (w * 2 + (p == 0 ? 1 : 0)) * kRows + y;
+      };
+      float acc[kCols][V], top = -INFINITY, sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = 0.0f;
-    if (on) {
-      auto slot = [&](int p) { return (p == 0 ? w0 * 2 + 1 : (w0 + p) * 2) * kRows + y; };
-      for (int p = first + sharing * lane; p < count; p += sharing * 32) top = fmaxf(top, parts.ml[slot(p)].x);
+      for (int j = 0; j < kCols; ++j)
 #pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const float base = top == -INFINITY ? 0.0f : top;
-#pragma unroll 8
-      for (int p = first; p < count; p += sharing) {
-        const int64_t at = slot(p);
-        const float2 ml = parts.ml[at];
-        const float f = ex2(ml.x - base);
-        sum = fmaf(f, ml.y, sum);
+        for (int i = 0; i < V; ++i) acc[j][i] = 0.0f;
+      // eight parts at a time, their loads together, under a running maximum
+      constexpr int kAhead = 8;
+      for (int p0 = 0; p0 < count; p0 += kAhead) {
+        float2 ml[kAhead];
+        float part[kAhead][kCols][V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] = fmaf(f, parts.o[at * D + i * 32 + lane], acc[i]);
-      }
-    }
+        for (int e = 0; e < kAhead; ++e) {
+          ml[e] = make_float2(-INFINITY, 0.0f);
+          if (p0 + e < count) {
+            const int64_t at = slot(p0 + e);
+            ml[e] = parts.ml[at];
 #pragma unroll
-    for (int i = 0; i < V; ++i) part_o[warp][i * 32 + lane] = acc[i];
-    if (lane == 0) part_ml[warp] = make_float2(top, sum);
-    __syncthreads();
-    if (on && first == 0) {
-      for (int w = warp; w < warp + sharing; ++w) top = fmaxf(top, part_ml[w].x);
-      const float base = top == -INFINITY ? 0.0f : top;
-      sum = 0.0f;
-      float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      float v2[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      for (int w = warp; w < warp + sharing; ++w) {
-        const float f = ex2(part_ml[w].x - base);
-        sum = fmaf(f, part_ml[w].y, sum);
-        if (4 * lane < D) {
+            for (int j = 0; j < kCols; ++j) {
+              const float* from = parts.o + at * D + j * 32 * V + lane * V;
+              if constexpr (V == 4) {
+                const float4 v = *reinterpret_cast<const float4*>(from);
+                part[e][j][0] = v.x, part[e][j][1] = v.y, part[e][j][2] = v.z, part[e][j][3] = v.w;
+              } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = fmaf(f, part_o[w][4 * lane + i], v[i]);
+                for (int i = 0; i < V; ++i) part[e][j][i] = from[i];
+              }
+            }
+          }
         }
-        if constexpr (D == 256) {
+        float now = top;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v2[i] = fmaf(f, part_o[w][128 + 4 * lane + i], v2[i]);
+        for (int e = 0; e < kAhead; ++e) now = fmaxf(now, ml[e].x);
+        const float base = now == -INFINITY ? 0.0f : now, f0 = ex2(top - base);
+        top = now;
+        sum *= f0;
+#pragma unroll
+        for (int j = 0; j < kCols; ++j)
+#pragma unroll
+          for (int i = 0; i < V; ++i) acc[j][i] *= f0;
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e) {
+          if (p0 + e < count) {
+            const float f = ex2(ml[e].x - base);
+            sum = fmaf(f, ml[e].y, sum);
+#pragma unroll
+            for (int j = 0; j < kCols; ++j)
+#pragma unroll
+              for (int i = 0; i < V; ++i) acc[j][i] = fmaf(f, part[e][j][i], acc[j][i]);
+          }
         }
       }
       const float inv = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
-      const int row = rec.row0 + y;
-      const int64_t at = ((int64_t)(r.row0 + row / g) * a.Hq + (int64_t)rec.h * g + row % g) * D + 4 * lane;
+      const int row = rec.row + y;
+      const int64_t at = ((int64_t)(rec.row0 + row / g) * a.Hq + (int64_t)rec.h * g + row % g) * D + lane * V;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] *= inv, v2[i] *= inv;
-      if (4 * lane < D) {
+      for (int j = 0; j < kCols; ++j) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[j][i] *= inv;
         if (a.o_bf16)
-          store_row<true>(a.o, at, v);
+          store_row<true>(a.o, at + j * 32 * V, acc[j]);
         else
-          store_row<false>(a.o, at, v);
-      }
-      if constexpr (D == 256) {
-        if (a.o_bf16)
-          store_row<true>(a.o, at + 128, v2);
-        else
-          store_row<false>(a.o, at + 128, v2);
+          store_row<false>(a.o, at + j * 32 * V, acc[j]);
       }
     }
-    __syncthreads();
+    dealt += rec.rows;
   }
 }
 
 template <int D, int NT, bool F32>
 cudaError_t launch(const KvAttentionArgs& a, cudaStream_t stream) {
   const unsigned grid = (unsigned)(sm100_host::sm_count() * blocks_per_sm(D, NT, F32));
-  constexpr int ring = kWarps * stages_of(D) * 2 * kTok * D;
+  constexpr int ring = kWarps * stages_of(D) * 2 * kStep * D;
   static std::atomic<bool> done[sm100_host::kMaxDevices];
   cudaError_t e = sm100_host::ensure_smem(kv_attention_kernel<D, NT, F32>, ring + (kMaxRequests + 1) * 8, done);
   if (e != cudaSuccess) return e;
   e = sm100_host::launch_pdl(kv_attention_kernel<D, NT, F32>, grid, kThreads, ring + (size_t)(a.B + 1) * 8, stream, 1, a);
   if (e != cudaSuccess) return e;
-  return sm100_host::launch_pdl(kv_attention_join_kernel<D, NT>, grid * kWarps, kJoinThreads, 0, stream, 1, a);
+  return sm100_host::launch_pdl(kv_attention_join_kernel<D, NT>, grid, kJoinThreads, 0, stream, 1, a);
 }
 
 template <int D>
