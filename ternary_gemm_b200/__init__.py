@@ -457,51 +457,54 @@ def hbl_gemv_ternary_dequant(A, packed, scales, alpha, y=None, y_dtype=None, str
 
 # ------------------------------------------------------------------ the paged 8-bit cache
 
-def _on_current(dtypes, **ts):
-    """Each tensor (None is passed over) on the current CUDA device, contiguous, of the dtype that `dtypes` names
-    for it (where it names one): the kernels take raw pointers and trust them."""
+# The calls below are made once per layer and token step, so their checks are few attribute reads per tensor.
+
+def _here(t) -> int:
+    """The device of t, which must be the current one (the kernels run there and take raw pointers)."""
+    dev = t.get_device()
+    if dev != _torch().cuda.current_device():
+        raise ValueError("tensors must be on the current CUDA device, got %s" % t.device)
+    return dev
+
+
+def _raw_stream(stream, dev: int) -> int:
     torch = _torch()
-    dev = torch.cuda.current_device()
-    for name, t in ts.items():
-        if t is None:
-            continue
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _demand(dev: int, *wanted):
+    """Each (name, tensor, dtype, shape) is contiguous, on device dev, of that dtype (None: any) and shape."""
+    for name, t, dtype, shape in wanted:
         if t.get_device() != dev:
-            raise ValueError("%s must be on the current CUDA device (%d)" % (name, dev))
+            raise ValueError("%s: expected a tensor on CUDA device %d, got %s" % (name, dev, t.device))
+        if dtype is not None and t.dtype is not dtype:
+            raise TypeError("%s: expected %s, got %s" % (name, dtype, t.dtype))
+        if t.shape != shape:
+            raise ValueError("%s: expected shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
         if not t.is_contiguous():
             raise ValueError("%s must be contiguous" % name)
-        want = dtypes.get(name)
-        if want is not None and t.dtype != want:
-            raise TypeError("%s: expected %s, got %s" % (name, want, t.dtype))
 
 
-def _shape(name, t, *shape):
-    if tuple(t.shape) != shape:
-        raise ValueError("%s: expected shape %s, got %s" % (name, shape, tuple(t.shape)))
-
-
-def _head_rows(name, t):
+def _head_rows(name, t, dev: int) -> int:
     """Rows of heads [T][H][D], heads and values contiguous, any row stride (columns of a wider matrix): the stride."""
-    torch = _torch()
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError("%s must be on the current CUDA device (%d)" % (name, torch.cuda.current_device()))
     if t.dim() != 3:
         raise ValueError("%s must be [rows][heads][head dimension]" % name)
-    T, H, D = t.shape
-    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+    (T, H, D), (row, head, value) = t.shape, t.stride()
+    if t.get_device() != dev:
+        raise ValueError("%s: expected a tensor on CUDA device %d, got %s" % (name, dev, t.device))
+    if (D > 1 and value != 1) or (H > 1 and head != D):
         raise ValueError("%s: heads and their values must be contiguous" % name)
-    return t.stride(0) if T > 1 else H * D
+    return row if T > 1 else H * D
 
 
-def _cache_shape(k_codes, k_scales, v_codes, v_scales):
+def _cache_shape(dev: int, k_codes, k_scales, v_codes, v_scales):
     torch = _torch()
-    _on_current({"k_codes": torch.uint8, "k_scales": torch.float32, "v_codes": torch.uint8, "v_scales": torch.float32},
-                k_codes=k_codes, k_scales=k_scales, v_codes=v_codes, v_scales=v_scales)
     if k_codes.dim() != 4:
         raise ValueError("k_codes must be [blocks][heads][block][head dimension]")
-    n, H, block, D = k_codes.shape
-    _shape("v_codes", v_codes, n, H, block, D)
-    _shape("k_scales", k_scales, n, H)
-    _shape("v_scales", v_scales, n, H)
+    shape = k_codes.shape
+    n, H, block, D = shape
+    _demand(dev, ("k_codes", k_codes, torch.uint8, shape), ("v_codes", v_codes, torch.uint8, shape),
+            ("k_scales", k_scales, torch.float32, (n, H)), ("v_scales", v_scales, torch.float32, (n, H)))
     return n, H, block, D
 
 
@@ -511,8 +514,7 @@ def hbl_kv_plan(cached, added, free_blocks, taken, table, block: int, T: int, to
     [B][width] (blocks from free_blocks, from place taken[0] on) and returns (total [B], row_start [B + 1],
     slots [T], positions [T], taken_out [1])."""
     torch = _torch()
-    i32 = torch.int32
-    names = ("cached", "added", "free_blocks", "taken", "table", "total", "row_start", "slots", "positions", "taken_out")
+    dev, i32 = _here(table), torch.int32
     B, width = table.shape
     new = lambda n: torch.empty((n,), dtype=i32, device=table.device)  # noqa: E731
     total = new(B) if total is None else total
@@ -520,16 +522,14 @@ def hbl_kv_plan(cached, added, free_blocks, taken, table, block: int, T: int, to
     slots = new(T) if slots is None else slots
     positions = new(T) if positions is None else positions
     taken_out = new(1) if taken_out is None else taken_out
-    _on_current(dict.fromkeys(names, i32), cached=cached, added=added, free_blocks=free_blocks, taken=taken, table=table,
-                total=total, row_start=row_start, slots=slots, positions=positions, taken_out=taken_out)
-    for name, t, n in (("cached", cached, B), ("added", added, B), ("taken", taken, 1), ("total", total, B),
-                       ("row_start", row_start, B + 1), ("slots", slots, T), ("positions", positions, T),
-                       ("taken_out", taken_out, 1)):
-        if t.numel() != n:
-            raise ValueError("%s: expected %d entries, got %d" % (name, n, t.numel()))
-    _check(lib().hbl_kv_plan(cached.data_ptr(), added.data_ptr(), B, block, free_blocks.data_ptr(), free_blocks.numel(),
+    one, free = (B,), free_blocks.numel()
+    _demand(dev, ("table", table, i32, (B, width)), ("cached", cached, i32, one), ("added", added, i32, one),
+            ("free_blocks", free_blocks, i32, (free,)), ("taken", taken, i32, (1,)), ("total", total, i32, one),
+            ("row_start", row_start, i32, (B + 1,)), ("slots", slots, i32, (T,)), ("positions", positions, i32, (T,)),
+            ("taken_out", taken_out, i32, (1,)))
+    _check(lib().hbl_kv_plan(cached.data_ptr(), added.data_ptr(), B, block, free_blocks.data_ptr(), free,
                              taken.data_ptr(), table.data_ptr(), width, T, total.data_ptr(), row_start.data_ptr(),
-                             slots.data_ptr(), positions.data_ptr(), taken_out.data_ptr(), _stream(stream)),
+                             slots.data_ptr(), positions.data_ptr(), taken_out.data_ptr(), _raw_stream(stream, dev)),
            "hbl_kv_plan")
     return total, row_start, slots, positions, taken_out
 
@@ -537,19 +537,18 @@ def hbl_kv_plan(cached, added, free_blocks, taken, table, block: int, T: int, to
 def hbl_kv_append(k, v, slots, k_codes, k_scales, v_codes, v_scales, bits: int = 8, stream=None):
     """Writes rows k, v [T][H][D] (float32/bf16; columns of a wider matrix are fine) into the cache at int32 slots [T]:
     codes uint8 [blocks][H][block][D], scales float32 [blocks][H], both in place.  Returns the four."""
-    torch = _torch()
-    n, H, block, D = _cache_shape(k_codes, k_scales, v_codes, v_scales)
-    ks, vs = _head_rows("k", k), _head_rows("v", v)
+    dev = _here(k_codes)
+    n, H, block, D = _cache_shape(dev, k_codes, k_scales, v_codes, v_scales)
+    ks, vs = _head_rows("k", k, dev), _head_rows("v", v, dev)
     T = k.shape[0]
-    _shape("k", k, T, H, D)
-    _shape("v", v, T, H, D)
-    if v.dtype != k.dtype:
+    if k.shape != (T, H, D) or v.shape != (T, H, D):
+        raise ValueError("k and v: expected shape %s, got %s and %s" % ((T, H, D), tuple(k.shape), tuple(v.shape)))
+    if v.dtype is not k.dtype:
         raise TypeError("k and v must have one dtype, got %s and %s" % (k.dtype, v.dtype))
-    _on_current({"slots": torch.int32}, slots=slots)
-    _shape("slots", slots, T)
+    _demand(dev, ("slots", slots, _torch().int32, (T,)))
     _check(lib().hbl_kv_append(k.data_ptr(), v.data_ptr(), _dtype_code(k), T, H, D, ks, vs, slots.data_ptr(), bits, n,
                                block, k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
-                               _stream(stream)), "hbl_kv_append")
+                               _raw_stream(stream, dev)), "hbl_kv_append")
     return k_codes, k_scales, v_codes, v_scales
 
 
@@ -564,26 +563,26 @@ def hbl_kv_attention(q, row_start, total, table, k_codes, k_scales, v_codes, v_s
     for 1/sqrt(D).  Returns o [T][Hq][D] (q's dtype unless o_dtype), rows outside the requests left as they were
     (zero in an o made here)."""
     torch = _torch()
-    n, Hkv, block, D = _cache_shape(k_codes, k_scales, v_codes, v_scales)
-    qs = _head_rows("q", q)
-    T, Hq = q.shape[0], q.shape[1]
-    _shape("q", q, T, Hq, D)
+    dev, i32 = _here(q), torch.int32
+    n, Hkv, block, D = _cache_shape(dev, k_codes, k_scales, v_codes, v_scales)
+    qs = _head_rows("q", q, dev)
+    T, Hq, Dq = q.shape
+    if Dq != D:
+        raise ValueError("q has head dimension %d, the cache %d" % (Dq, D))
     B, width = table.shape
     if o is None:
         o = torch.zeros((T, Hq, D), dtype=o_dtype or q.dtype, device=q.device)
     if workspace is None:
         workspace = torch.empty((hbl_kv_attention_workspace_bytes(T, Hq, Hkv, D, B),), dtype=torch.uint8, device=q.device)
-    i32 = torch.int32
-    _on_current({"row_start": i32, "total": i32, "table": i32, "scale": torch.float32}, row_start=row_start, total=total,
-                table=table, scale=scale, o=o, workspace=workspace)
-    _shape("o", o, T, Hq, D)
-    _shape("row_start", row_start, B + 1)
-    _shape("total", total, B)
+    _demand(dev, ("row_start", row_start, i32, (B + 1,)), ("total", total, i32, (B,)), ("table", table, i32, (B, width)),
+            ("o", o, None, (T, Hq, D)), ("workspace", workspace, None, workspace.shape))
+    if scale is not None:
+        _demand(dev, ("scale", scale, torch.float32, (1,)))
     _check(lib().hbl_kv_attention(q.data_ptr(), _dtype_code(q), T, qs, Hq, Hkv, D, row_start.data_ptr(), total.data_ptr(),
                                   B, table.data_ptr(), width, n, block, bits, k_codes.data_ptr(), k_scales.data_ptr(),
                                   v_codes.data_ptr(), v_scales.data_ptr(), None if scale is None else scale.data_ptr(),
-                                  o.data_ptr(), _dtype_code(o), workspace.data_ptr(),
-                                  workspace.numel() * workspace.element_size(), _stream(stream)), "hbl_kv_attention")
+                                  o.data_ptr(), _dtype_code(o), workspace.data_ptr(), workspace.nbytes,
+                                  _raw_stream(stream, dev)), "hbl_kv_attention")
     return o
 
 
@@ -597,23 +596,22 @@ def hbl_add_rms_quant(x, bits: int, residual=None, gain=None, h=None, codes=None
     """h = x + residual, then RMSNorm with a float32 gain [K] and the per-token quantizer (bits 8 absmax, 4 absmean):
     (h [M][K] of x's dtype, int8 codes [M][K], float32 scales [M]).  h may be x or residual itself."""
     torch = _torch()
-    M, K = x.shape
+    dev, dtype, shape = _here(x), x.dtype, x.shape
+    M, K = shape
     if h is None:
         h = torch.empty_like(x)
     if codes is None:
         codes = torch.empty((M, K), dtype=torch.int8, device=x.device)
     if scales is None:
         scales = torch.empty((M,), dtype=torch.float32, device=x.device)
-    _on_current({"residual": x.dtype, "gain": torch.float32, "h": x.dtype, "codes": torch.int8, "scales": torch.float32},
-                x=x, residual=residual, gain=gain, h=h, codes=codes, scales=scales)
-    for name, t in (("residual", residual), ("h", h), ("codes", codes)):
-        if t is not None:
-            _shape(name, t, M, K)
-    _shape("scales", scales, M)
+    _demand(dev, ("x", x, dtype, shape), ("h", h, dtype, shape), ("codes", codes, torch.int8, shape),
+            ("scales", scales, torch.float32, (M,)))
+    if residual is not None:
+        _demand(dev, ("residual", residual, dtype, shape))
     if gain is not None:
-        _shape("gain", gain, K)
+        _demand(dev, ("gain", gain, torch.float32, (K,)))
     _check(lib().hbl_add_rms_quant(x.data_ptr(), _opt(residual), _dtype_code(x), M, K, _opt(gain), bits, h.data_ptr(),
-                                   codes.data_ptr(), scales.data_ptr(), _stream(stream)), "hbl_add_rms_quant")
+                                   codes.data_ptr(), scales.data_ptr(), _raw_stream(stream, dev)), "hbl_add_rms_quant")
     return h, codes, scales
 
 
@@ -626,26 +624,25 @@ def hbl_add_rms_quant_backward(h, g_t, gain=None, g_h=None, g_x=None, g_gain=Non
     (h's dtype) along the residual stream.  Returns (g_x [M][K] of h's dtype, for x and residual alike; g_gain
     float32 [K], None without a gain)."""
     torch = _torch()
-    M, K = h.shape
+    dev, dtype, shape, f32 = _here(h), h.dtype, h.shape, torch.float32
+    M, K = shape
     if g_x is None:
         g_x = torch.empty_like(h)
     if g_gain is None and gain is not None:
-        g_gain = torch.empty((K,), dtype=torch.float32, device=h.device)
+        g_gain = torch.empty((K,), dtype=f32, device=h.device)
     if workspace is None:
         workspace = torch.empty((hbl_add_rms_quant_backward_workspace_bytes(M, K),), dtype=torch.uint8, device=h.device)
-    f32 = torch.float32
-    _on_current({"gain": f32, "g_h": h.dtype, "g_x": h.dtype, "g_gain": f32}, h=h, g_t=g_t, gain=gain, g_h=g_h, g_x=g_x,
-                g_gain=g_gain, workspace=workspace)
-    for name, t in (("g_t", g_t), ("g_h", g_h), ("g_x", g_x)):
-        if t is not None:
-            _shape(name, t, M, K)
+    _demand(dev, ("h", h, dtype, shape), ("g_t", g_t, None, shape), ("g_x", g_x, dtype, shape),
+            ("workspace", workspace, None, workspace.shape))
+    if g_h is not None:
+        _demand(dev, ("g_h", g_h, dtype, shape))
     for name, t in (("gain", gain), ("g_gain", g_gain)):
         if t is not None:
-            _shape(name, t, K)
+            _demand(dev, (name, t, f32, (K,)))
     _check(lib().hbl_add_rms_quant_backward(h.data_ptr(), _dtype_code(h), M, K, _opt(gain), g_t.data_ptr(),
                                             _dtype_code(g_t), _opt(g_h), g_x.data_ptr(), _opt(g_gain),
-                                            workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                            _stream(stream)), "hbl_add_rms_quant_backward")
+                                            workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, dev)),
+           "hbl_add_rms_quant_backward")
     return g_x, g_gain
 
 

@@ -74,155 +74,286 @@ __device__ __forceinline__ void store8(void* p, int64_t i, const float (&v)[8]) 
   }
 }
 
-template <typename S, bool BF16, int BITS>
-__global__ void __launch_bounds__(S::kThreads)
+// The rows that a CTA takes next are on their way while it works on one: a
+// thread copies into shared memory the vectors that it will read itself, so
+// that its own wait is all the ordering there is, and the copies hold no
+// registers.
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// a vector (eight values) of this thread: its place in the ring
+template <typename S, bool BF16>
+__device__ __forceinline__ uint32_t slot_of(uint32_t row, int tensor, int j) {
+  return row + ((tensor * S::E + j) * (BF16 ? 1 : 2)) * (16 * S::kThreads) + threadIdx.x * 16;
+}
+template <typename S, bool BF16>
+__device__ __forceinline__ void copy8(uint32_t slot, const void* p, int64_t i) {
+  const char* from = reinterpret_cast<const char*>(p) + i * (BF16 ? 2 : 4);
+  cp_async16(slot, from);
+  if constexpr (!BF16) cp_async16(slot + 16 * S::kThreads, from + 16);
+}
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+template <typename S, bool BF16>
+__device__ __forceinline__ void take8(uint32_t slot, float (&v)[8]) {
+  const uint4 a = lds128(slot);
+  if constexpr (BF16) {
+    rowkit::bf16x8_to_f32(a, v);
+  } else {
+    const uint4 b = lds128(slot + 16 * S::kThreads);
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(w[e]);
+  }
+}
+
+// the gain of this thread's vectors, held where 32 values a thread leave room
+template <typename S>
+__device__ __forceinline__ void load_gain(const float* gain, int j, int vectors, float (&w)[8]) {
+  const int i = j * S::T + threadIdx.x % S::T;
+  if (gain && i < vectors) {
+    rowkit::load8<false>(gain, i * 8, w);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = 1.0f;
+  }
+}
+
+// CTAs per SM and rows in shared memory per CTA for rows of `bytes` over all
+// the tensors that are copied: as many CTAs as their registers allow (at most
+// 128 a thread) while two rows each fit, a third where it fits too; rows that
+// do not fit twice are read straight into registers (no stages).
+struct Flow {
+  int blocks, stages;
+};
+constexpr int most_blocks(int threads) { return 512 / threads; }
+constexpr Flow flow_for(int threads, int bytes) {
+  const int room = 224 * 1024;
+  for (int blocks = most_blocks(threads); blocks >= 1; blocks /= 2)
+    for (int stages = 3; stages >= 2; --stages)
+      if (blocks * stages * bytes <= room) return {blocks, stages};
+  return {most_blocks(threads), 0};
+}
+
+// kStages 0: a CTA per S::R rows, read straight into registers; else a grid
+// that stays, its rows copied kStages - 1 ahead
+template <typename S, bool BF16, int BITS, int kStages, int kBlocks>
+__global__ void __launch_bounds__(S::kThreads, kBlocks)
 add_rms_quant_kernel(const void* x, const void* residual, int64_t M, int K, const float* __restrict__ gain, void* h,
                      int8_t* codes, float* scales) {
   constexpr int T = S::T, E = S::E, WPR = S::kWarpsPerRow;
-  __shared__ double red_d[2][S::R * WPR];
-  __shared__ float red_f[S::R * WPR];
+  constexpr uint32_t kRow = 2 * E * S::kThreads * (BF16 ? 16 : 32);
+  extern __shared__ __align__(16) uint8_t ring_bytes[];
+  __shared__ double red_d[2][2][S::R * WPR];
+  __shared__ float red_f[2][S::R * WPR];
   const int rl = threadIdx.x / T, t = threadIdx.x % T;
-  const int64_t row = (int64_t)blockIdx.x * S::R + rl;
-  const bool active = row < M;
-  const int64_t base = (active ? row : 0) * K;
   const int vectors = K / 8;
+  const int64_t step = (int64_t)gridDim.x * S::R;
+  const uint32_t ring = sm100::smem_u32(ring_bytes);
 
-  float v[E][8];
-  double ss = 0.0;
+  float w[kStages > 0 ? E : 1][8];
+  if constexpr (kStages > 0) {
 #pragma unroll
-  for (int j = 0; j < E; ++j) {
-    const int i = j * T + t;
-    if (active && i < vectors) {
-      load8<BF16>(x, base + i * 8, v[j]);
-      if (residual) {
-        float r[8];
-        load8<BF16>(residual, base + i * 8, r);
+    for (int j = 0; j < E; ++j) load_gain<S>(gain, j, vectors, w[j]);
+  }
+  auto fetch = [&](int64_t row, uint32_t at) {
+    if (row < M) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[j][e] = __fadd_rn(v[j][e], r[e]);
-        if constexpr (BF16) rowkit::bf16x8_to_f32(bf16x8(v[j]), v[j]);
+      for (int j = 0; j < E; ++j) {
+        const int i = j * T + t;
+        if (i < vectors) {
+          copy8<S, BF16>(slot_of<S, BF16>(at, 0, j), x, row * K + i * 8);
+          if (residual) copy8<S, BF16>(slot_of<S, BF16>(at, 1, j), residual, row * K + i * 8);
+        }
       }
-    } else {
+    }
+    cp_commit();
+  };
+  int64_t row = (int64_t)blockIdx.x * S::R + rl;
+  uint32_t here = ring, next = ring;
+  if constexpr (kStages > 0) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[j][e] = 0.0f;
+    for (int i = 0; i < kStages - 1; ++i) {
+      fetch(row + i * step, next);
+      next += kRow;
     }
   }
-#pragma unroll
-  for (int j = 0; j < E; ++j) {
-    const int i = j * T + t;
-    if (h && active && i < vectors) store8<BF16>(h, base + i * 8, v[j]);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fma((double)v[j][e], (double)v[j][e], ss);
-  }
-  ss = RowReduce<T, WPR>::run(ss, AddD(), red_d[0], rl, t);
-  const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn((float)(ss / (double)K), 1e-5f)));
-  float top = 0.0f;
-  double sum = 0.0;
-#pragma unroll
-  for (int j = 0; j < E; ++j) {
-    const int i = j * T + t;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[j][e] = __fmul_rn(v[j][e], rstd);
-    if (gain && i < vectors) {
-      float w[8];
-      rowkit::load8<false>(gain, i * 8, w);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[j][e] = __fmul_rn(v[j][e], w[e]);
+  int parity = 0;
+  for (int64_t row0 = (int64_t)blockIdx.x * S::R; row0 < M; row0 += step, row += step, parity ^= 1) {
+    const bool active = row < M;
+    const int64_t base = (active ? row : 0) * K;
+    if constexpr (kStages > 0) {
+      fetch(row + (kStages - 1) * step, next);
+      next = next == ring + (kStages - 1) * kRow ? ring : next + kRow;
+      cp_wait<kStages - 1>();
     }
+    float v[E][8];
+    double ss = 0.0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      if constexpr (BITS == 8)
-        top = fmaxf(top, fabsf(v[j][e]));
-      else
-        sum += q::abs_f64(v[j][e]);
+    for (int j = 0; j < E; ++j) {
+      const int i = j * T + t;
+      if (active && i < vectors) {
+        if constexpr (kStages > 0)
+          take8<S, BF16>(slot_of<S, BF16>(here, 0, j), v[j]);
+        else
+          load8<BF16>(x, base + i * 8, v[j]);
+        if (residual) {
+          float r[8];
+          if constexpr (kStages > 0)
+            take8<S, BF16>(slot_of<S, BF16>(here, 1, j), r);
+          else
+            load8<BF16>(residual, base + i * 8, r);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[j][e] = __fadd_rn(v[j][e], r[e]);
+          if constexpr (BF16) rowkit::bf16x8_to_f32(bf16x8(v[j]), v[j]);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[j][e] = 0.0f;
+      }
     }
-  }
-  q::RowParams p;
-  if constexpr (BITS == 8)
-    p = q::params_int8(RowReduce<T, WPR>::run(top, MaxF(), red_f, rl, t));
-  else
-    p = q::params_int4(RowReduce<T, WPR>::run(sum, AddD(), red_d[1], rl, t), K);
-  if (!active) return;
-  if (t == 0) scales[row] = p.scale();
+    if constexpr (kStages > 0) here = here == ring + (kStages - 1) * kRow ? ring : here + kRow;
 #pragma unroll
-  for (int j = 0; j < E; ++j) {
-    const int i = j * T + t;
-    uint32_t m[8];
+    for (int j = 0; j < E; ++j) {
+      const int i = j * T + t;
+      if (h && active && i < vectors) store8<BF16>(h, base + i * 8, v[j]);
 #pragma unroll
-    for (int e = 0; e < 8; e += 2) rowkit::magic2(v[j][e], v[j][e + 1], p.r, m[e], m[e + 1]);
-    if constexpr (BITS == 4) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) m[e] = q::clip_magic_int4(m[e]);
+      for (int e = 0; e < 8; ++e) ss = fma((double)v[j][e], (double)v[j][e], ss);
     }
-    if (i < vectors)
-      *reinterpret_cast<uint2*>(codes + base + i * 8) =
-          make_uint2(q::gather_low_bytes(m[0], m[1], m[2], m[3]), q::gather_low_bytes(m[4], m[5], m[6], m[7]));
+    ss = RowReduce<T, WPR>::run(ss, AddD(), red_d[parity][0], rl, t);
+    const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn((float)(ss / (double)K), 1e-5f)));
+    float top = 0.0f;
+    double sum = 0.0;
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      if constexpr (kStages == 0) load_gain<S>(gain, j, vectors, w[0]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v[j][e] = __fmul_rn(__fmul_rn(v[j][e], rstd), w[kStages > 0 ? j : 0][e]);  // times 1 is exact
+        if constexpr (BITS == 8)
+          top = fmaxf(top, fabsf(v[j][e]));
+        else
+          sum += q::abs_f64(v[j][e]);
+      }
+    }
+    q::RowParams p;
+    if constexpr (BITS == 8)
+      p = q::params_int8(RowReduce<T, WPR>::run(top, MaxF(), red_f[parity], rl, t));
+    else
+      p = q::params_int4(RowReduce<T, WPR>::run(sum, AddD(), red_d[parity][1], rl, t), K);
+    if (!active) continue;
+    if (t == 0) scales[row] = p.scale();
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      const int i = j * T + t;
+      uint32_t m[8];
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) rowkit::magic2(v[j][e], v[j][e + 1], p.r, m[e], m[e + 1]);
+      if constexpr (BITS == 4) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m[e] = q::clip_magic_int4(m[e]);
+      }
+      if (i < vectors)
+        *reinterpret_cast<uint2*>(codes + base + i * 8) =
+            make_uint2(q::gather_low_bytes(m[0], m[1], m[2], m[3]), q::gather_low_bytes(m[4], m[5], m[6], m[7]));
+    }
   }
 }
 
 // ---------------------------------------------------------------- gradient
 
-// CTAs per SM of the gradient: its registers hold h, g_t and the gain's sums
-template <typename S>
-constexpr int grad_blocks() {
-  return S::E > 4 ? 1 : (S::kThreads <= 128 ? 3 : (S::kThreads <= 256 ? 2 : 1));
-}
-
-template <typename S, bool BF16, bool GT16>
-__global__ void __launch_bounds__(S::kThreads, grad_blocks<S>())
+// A grid that stays: a thread's columns of the gain's sums stay in registers
+// over its rows.  kStages as above (three tensors a row).
+template <typename S, bool BF16, bool GT16, int kStages, int kBlocks>
+__global__ void __launch_bounds__(S::kThreads, kBlocks)
 add_rms_grad_kernel(const void* __restrict__ h, int64_t M, int K, const float* __restrict__ gain,
                     const void* __restrict__ g_t, const void* g_h, void* g_x, float* __restrict__ sums) {
   constexpr int T = S::T, E = S::E, WPR = S::kWarpsPerRow;
-  constexpr bool kHold = E <= 4;  // longer rows are read again (from L2) for their outputs
+  constexpr bool kRinged = kStages > 0, kGain = kRinged && E <= 4;
+  constexpr uint32_t kH = E * S::kThreads * (BF16 ? 16 : 32), kT = E * S::kThreads * (GT16 ? 16 : 32);
+  constexpr uint32_t kRow = 2 * kH + kT;  // h, g_h, g_t
+  extern __shared__ __align__(16) uint8_t ring_bytes[];
   __shared__ float2 red[2][S::R * WPR];
   const int rl = threadIdx.x / T, t = threadIdx.x % T;
   const int vectors = K / 8;
   const float inv_k = __fdiv_rn(1.0f, (float)K);
-  float acc[E][8];
+  const int64_t step = (int64_t)gridDim.x * S::R;
+  const uint32_t ring = sm100::smem_u32(ring_bytes);
+  float acc[E][8], w[kGain ? E : 1][8];
 #pragma unroll
-  for (int j = 0; j < E; ++j)
+  for (int j = 0; j < E; ++j) {
+    if constexpr (kGain) load_gain<S>(gain, j, vectors, w[j]);
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[j][e] = 0.0f;
-
+  }
+  auto fetch = [&](int64_t row, uint32_t at) {
+    if (row < M) {
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        const int i = j * T + t;
+        if (i < vectors) {
+          copy8<S, BF16>(slot_of<S, BF16>(at, 0, j), h, row * K + i * 8);
+          copy8<S, GT16>(slot_of<S, GT16>(at + 2 * kH, 0, j), g_t, row * K + i * 8);
+          if (g_h) copy8<S, BF16>(slot_of<S, BF16>(at, 1, j), g_h, row * K + i * 8);
+        }
+      }
+    }
+    cp_commit();
+  };
+  int64_t row = (int64_t)blockIdx.x * S::R + rl;
+  uint32_t here = ring, next = ring;
+  if constexpr (kRinged) {
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) {
+      fetch(row + i * step, next);
+      next += kRow;
+    }
+  }
   int parity = 0;
-  for (int64_t row0 = (int64_t)blockIdx.x * S::R; row0 < M; row0 += (int64_t)gridDim.x * S::R, parity ^= 1) {
-    const bool active = row0 + rl < M;
-    const int64_t base = (active ? row0 + rl : 0) * K;
-    float a[kHold ? E : 1][8], g[kHold ? E : 1][8];
-    float ss = 0.0f, dot = 0.0f;
+  for (int64_t row0 = (int64_t)blockIdx.x * S::R; row0 < M; row0 += step, row += step, parity ^= 1) {
+    const bool active = row < M;
+    const int64_t base = (active ? row : 0) * K;
+    if constexpr (kRinged) {
+      fetch(row + (kStages - 1) * step, next);
+      next = next == ring + (kStages - 1) * kRow ? ring : next + kRow;
+      cp_wait<kStages - 1>();
+    }
     auto read = [&](int j, float (&hv)[8], float (&gv)[8]) {
       const int i = j * T + t;
       if (active && i < vectors) {
-        load8<BF16>(h, base + i * 8, hv);
-        load8<GT16>(g_t, base + i * 8, gv);
+        if constexpr (kRinged) {
+          take8<S, BF16>(slot_of<S, BF16>(here, 0, j), hv);
+          take8<S, GT16>(slot_of<S, GT16>(here + 2 * kH, 0, j), gv);
+        } else {
+          load8<BF16>(h, base + i * 8, hv);
+          load8<GT16>(g_t, base + i * 8, gv);
+        }
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) hv[e] = gv[e] = 0.0f;
       }
     };
-    auto gains = [&](int j, float (&w)[8]) {
-      const int i = j * T + t;
-      if (gain && i < vectors) {
-        rowkit::load8<false>(gain, i * 8, w);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = 1.0f;
-      }
-    };
-    if constexpr (kHold) {
-#pragma unroll
-      for (int j = 0; j < E; ++j) read(j, a[j], g[j]);
-    }
+    // both passes over the row read it from the ring (without one: from L2 the second time)
+    float ss = 0.0f, dot = 0.0f;
 #pragma unroll
     for (int j = 0; j < E; ++j) {
-      float w[8];
-      gains(j, w);
-      if constexpr (!kHold) read(j, a[0], g[0]);
-      float s = 0.0f, d = 0.0f;
+      float hv[8], gv[8], s = 0.0f, d = 0.0f;
+      read(j, hv, gv);
+      if constexpr (!kGain) load_gain<S>(gain, j, vectors, w[0]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float hv = a[kHold ? j : 0][e];
-        s = fmaf(hv, hv, s);
-        d = fmaf(g[kHold ? j : 0][e] * w[e], hv, d);
+        s = fmaf(hv[e], hv[e], s);
+        d = fmaf(gv[e] * w[kGain ? j : 0][e], hv[e], d);
       }
       ss += s;
       dot += d;
@@ -237,8 +368,8 @@ add_rms_grad_kernel(const void* __restrict__ h, int64_t M, int K, const float* _
       __syncthreads();
       ss = dot = 0.0f;
 #pragma unroll
-      for (int w = 0; w < WPR; ++w) {
-        const float2 r = red[parity][rl * WPR + w];
+      for (int i = 0; i < WPR; ++i) {
+        const float2 r = red[parity][rl * WPR + i];
         ss += r.x;
         dot += r.y;
       }
@@ -248,25 +379,30 @@ add_rms_grad_kernel(const void* __restrict__ h, int64_t M, int K, const float* _
 #pragma unroll
     for (int j = 0; j < E; ++j) {
       const int i = j * T + t;
-      float w[8], out[8];
-      gains(j, w);
-      if constexpr (!kHold) read(j, a[0], g[0]);
       const bool there = active && i < vectors;
+      float hv[8], gv[8], out[8];
+      read(j, hv, gv);
+      if constexpr (!kGain) load_gain<S>(gain, j, vectors, w[0]);
       if (g_h && there) {
-        load8<BF16>(g_h, base + i * 8, out);
+        if constexpr (kRinged)
+          take8<S, BF16>(slot_of<S, BF16>(here, 1, j), out);
+        else
+          load8<BF16>(g_h, base + i * 8, out);
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) out[e] = 0.0f;
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float n = a[kHold ? j : 0][e] * rstd, gv = g[kHold ? j : 0][e];
-        acc[j][e] = fmaf(gv, n, acc[j][e]);
-        out[e] = fmaf(rstd, fmaf(-n, c, gv * w[e]), out[e]);
+        const float n = hv[e] * rstd;
+        acc[j][e] = fmaf(gv[e], n, acc[j][e]);
+        out[e] = fmaf(rstd, fmaf(-n, c, gv[e] * w[kGain ? j : 0][e]), out[e]);
       }
       if (there) store8<BF16>(g_x, base + i * 8, out);
     }
+    if constexpr (kRinged) here = here == ring + (kStages - 1) * kRow ? ring : here + kRow;
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the sum over CTAs waits for the grid's end
   if (!sums) return;
 #pragma unroll
   for (int j = 0; j < E; ++j) {
@@ -275,25 +411,26 @@ add_rms_grad_kernel(const void* __restrict__ h, int64_t M, int K, const float* _
   }
 }
 
-// g_gain[k] = sum of the partial sums [count][K]: 32 columns per CTA, eight
-// warps on every eighth row
-__global__ void __launch_bounds__(256) gain_sum_kernel(const float* __restrict__ sums, int count, int K, float* g_gain) {
-  __shared__ float part[8][33];
+// g_gain[k] = sum of the partial sums [count][K]: 32 columns per CTA, 32 warps
+// on every 32nd row (the partial sums are in L2: round trips are what counts)
+constexpr int kSumWarps = 32;
+__global__ void __launch_bounds__(kSumWarps * 32)
+gain_sum_kernel(const float* sums, int count, int K, float* g_gain) {
+  __shared__ float part[kSumWarps][33];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = blockIdx.x * 32 + lane;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   float s = 0.0f;
   if (k < K) {
 #pragma unroll 8
-    for (int i = warp; i < count; i += 8) s += sums[(int64_t)i * K + k];
+    for (int i = warp; i < count; i += kSumWarps) s += sums[(int64_t)i * K + k];
   }
   part[warp][lane] = s;
   __syncthreads();
-  if (warp == 0 && k < K) {
-    s = 0.0f;
+  s = part[lane][warp];
 #pragma unroll
-    for (int w = 0; w < 8; ++w) s += part[w][lane];
-    g_gain[k] = s;
-  }
+  for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  const int to = blockIdx.x * 32 + warp;
+  if (lane == 0 && to < K) g_gain[to] = s;
 }
 
 // f(Rows<T, E>()) for the rows of K values
@@ -307,10 +444,50 @@ cudaError_t by_length(int64_t K, F&& f) {
   return f(Rows<512, 8>());
 }
 
+template <typename Kernel, typename... Args>
+cudaError_t start(Kernel kernel, std::atomic<bool> (&done)[sm100_host::kMaxDevices], int64_t grid, int threads, int smem,
+                  cudaStream_t stream, Args... args) {
+  if (smem) {
+    cudaError_t e = sm100_host::ensure_smem(kernel, smem, done);
+    if (e != cudaSuccess) return e;
+  }
+  kernel<<<(unsigned)grid, threads, smem, stream>>>(args...);
+  return cudaGetLastError();
+}
+
 template <typename S>
-int64_t grad_grid(int64_t M) {
-  const int64_t need = (M + S::R - 1) / S::R, cap = (int64_t)sm100_host::sm_count() * grad_blocks<S>();
+int64_t staying_grid(int64_t M, int blocks) {
+  const int64_t need = (M + S::R - 1) / S::R, cap = (int64_t)sm100_host::sm_count() * blocks;
   return need < cap ? need : cap;
+}
+
+template <typename S, bool BF16, int BITS>
+cudaError_t launch_quant(const void* x, const void* residual, int64_t M, int64_t K, const float* gain, void* h,
+                         int8_t* codes, float* scales, cudaStream_t stream) {
+  constexpr int row_bytes = 2 * S::E * S::kThreads * (BF16 ? 16 : 32);
+  constexpr Flow flow = flow_for(S::kThreads, row_bytes);
+  static std::atomic<bool> done[sm100_host::kMaxDevices];
+  const int64_t need = (M + S::R - 1) / S::R, grid = staying_grid<S>(M, flow.blocks);
+  // less than two rounds of the staying grid: nothing to copy ahead
+  if (flow.stages == 0 || need < 2 * grid)
+    return start(add_rms_quant_kernel<S, BF16, BITS, 0, most_blocks(S::kThreads)>, done, need, S::kThreads, 0, stream, x,
+                 residual, M, (int)K, gain, h, codes, scales);
+  return start(add_rms_quant_kernel<S, BF16, BITS, flow.stages, flow.blocks>, done, grid, S::kThreads,
+               flow.stages * row_bytes, stream, x, residual, M, (int)K, gain, h, codes, scales);
+}
+
+template <typename S, bool BF16, bool GT16>
+cudaError_t launch_grad(const void* h, int64_t M, int64_t K, const float* gain, const void* g_t, const void* g_h,
+                        void* g_x, float* g_gain, float* sums, cudaStream_t stream) {
+  constexpr int row_bytes = S::E * S::kThreads * (2 * (BF16 ? 16 : 32) + (GT16 ? 16 : 32));
+  constexpr Flow flow = flow_for(S::kThreads, row_bytes);
+  static std::atomic<bool> done[sm100_host::kMaxDevices];
+  const int64_t grid = staying_grid<S>(M, flow.blocks);
+  cudaError_t e = start(add_rms_grad_kernel<S, BF16, GT16, flow.stages, flow.blocks>, done, grid, S::kThreads,
+                        flow.stages * row_bytes, stream, h, M, (int)K, gain, g_t, g_h, g_x, g_gain ? sums : nullptr);
+  if (e != cudaSuccess || !g_gain) return e;
+  return sm100_host::launch_pdl(gain_sum_kernel, (unsigned)((K + 31) / 32), kSumWarps * 32, 0, stream, 1, (const float*)sums,
+                                (int)(grid * S::R), (int)K, g_gain);
 }
 
 }  // namespace
@@ -320,11 +497,9 @@ cudaError_t launch_add_rms_quant(const void* x, const void* residual, bool bf16,
                                  cudaStream_t stream) {
   return by_length(K, [&](auto rows) {
     using S = decltype(rows);
-    const unsigned grid = (unsigned)((M + S::R - 1) / S::R);
-    auto kernel = bf16 ? (bits == 8 ? add_rms_quant_kernel<S, true, 8> : add_rms_quant_kernel<S, true, 4>)
-                       : (bits == 8 ? add_rms_quant_kernel<S, false, 8> : add_rms_quant_kernel<S, false, 4>);
-    kernel<<<grid, S::kThreads, 0, stream>>>(x, residual, M, (int)K, gain, h, codes, scales);
-    return cudaGetLastError();
+    auto go = bf16 ? (bits == 8 ? launch_quant<S, true, 8> : launch_quant<S, true, 4>)
+                   : (bits == 8 ? launch_quant<S, false, 8> : launch_quant<S, false, 4>);
+    return go(x, residual, M, K, gain, h, codes, scales, stream);
   });
 }
 
@@ -332,7 +507,7 @@ size_t add_rms_backward_workspace(int64_t M, int64_t K) {
   size_t bytes = 0;
   by_length(K, [&](auto rows) {
     using S = decltype(rows);
-    bytes = (size_t)grad_grid<S>(M) * S::R * (size_t)K * 4;
+    bytes = (size_t)staying_grid<S>(M, most_blocks(S::kThreads)) * S::R * (size_t)K * 4;
     return cudaSuccess;
   });
   return bytes;
@@ -343,15 +518,9 @@ cudaError_t launch_add_rms_quant_backward(const void* h, bool bf16, int64_t M, i
                                           void* workspace, cudaStream_t stream) {
   return by_length(K, [&](auto rows) {
     using S = decltype(rows);
-    const int64_t grid = grad_grid<S>(M);
-    float* sums = g_gain ? reinterpret_cast<float*>(workspace) : nullptr;
-    auto kernel = bf16 ? (gt_bf16 ? add_rms_grad_kernel<S, true, true> : add_rms_grad_kernel<S, true, false>)
-                       : (gt_bf16 ? add_rms_grad_kernel<S, false, true> : add_rms_grad_kernel<S, false, false>);
-    kernel<<<(unsigned)grid, S::kThreads, 0, stream>>>(h, M, (int)K, gain, g_t, g_h, g_x, sums);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || !g_gain) return e;
-    return sm100_host::launch_pdl(gain_sum_kernel, (unsigned)((K + 31) / 32), 256, 0, stream, 1, (const float*)sums,
-                                  (int)(grid * S::R), (int)K, g_gain);
+    auto go = bf16 ? (gt_bf16 ? launch_grad<S, true, true> : launch_grad<S, true, false>)
+                   : (gt_bf16 ? launch_grad<S, false, true> : launch_grad<S, false, false>);
+    return go(h, M, K, gain, g_t, g_h, g_x, g_gain, reinterpret_cast<float*>(workspace), stream);
   });
 }
 
