@@ -545,7 +545,7 @@ hbl_status hbl_kv_append(const void* k, const void* v, hbl_dtype xt, int64_t T, 
 
 size_t hbl_kv_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t B) {
   if (check_rows(T) != HBL_OK || check_heads(Hq, Hkv) != HBL_OK || check_head_dim(D) != HBL_OK ||
-      check_requests(B, 1) != HBL_OK)
+      check_requests(B, 1) != HBL_OK || T * Hq > INT32_MAX)
     return 0;
   return hbl::kv_attention_workspace(T, (int)Hq, (int)Hkv, (int)D, (int)B);
 }
@@ -568,6 +568,7 @@ hbl_status hbl_kv_attention(const void* q, hbl_dtype qt, int64_t T, int64_t q_st
   if ((s = check_head_dim(D)) != HBL_OK) return s;
   if ((s = check_rows(T)) != HBL_OK) return s;
   if ((s = check_requests(B, width)) != HBL_OK) return s;
+  if (T * Hq > INT32_MAX) return HBL_ERR_UNSUPPORTED;  // rows of a request are counted in 32 bits
   if ((s = check_cache(num_blocks, block, bits)) != HBL_OK) return s;
   if ((s = check_row_stride(q_stride, Hq, D, qt)) != HBL_OK) return s;
   if (!workspace || !aligned(workspace, 256) ||

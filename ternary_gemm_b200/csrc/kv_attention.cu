@@ -886,6 +886,7 @@ size_t kv_attention_workspace(int64_t T, int Hq, int Hkv, int D, int B) {
 }
 
 cudaError_t launch_kv_attention(const KvAttentionArgs& a, cudaStream_t stream) {
+  if (kv_attention_prompt_supports(a)) return launch_kv_attention_prompt(a, stream);
   switch (a.D) {
     case 32: return launch_d<32>(a, stream);
     case 64: return launch_d<64>(a, stream);

@@ -1,0 +1,607 @@
+// Causal attention over the paged 8-bit cache for many rows per request
+// (prompts and chunks of them): bf16 queries, head dimension 64 or 128.
+//
+// The arithmetic is that of kv_attention.cu: centred codes k' = k - z and
+// v' = v - z enter the products exactly as fp16,
+//
+//   s_j = scale u_k(j) (2 sum_d q_d k'_jd + sum_d q_d)
+//   w_j = exp(s_j) u_v(j),   o = sum_j w_j (2 v'_j + 1) / sum_j w_j / u_v(j)
+//
+// and the weights are held on a scale where a row's largest lies in
+// [2^11, 2^15]: the scale follows the running maximum only when that grew by
+// more than four powers of two, so the accumulator in tensor memory is seldom
+// rescaled, and fp16 keeps 11 bits of all weights down to 2^-25 of the largest.
+//
+// Rows are many, so this is a matter of the tensor cores: a CTA takes 256 rows
+// of one cached head (two tiles of 128, query heads of the group times the
+// request's rows) over tiles of 128 tokens.
+//   warps 0-3, 4-7  softmax of the first and the second row tile, a row per
+//                   thread: scores from tensor memory, weights back into it
+//   warps 8-11      codes from the pages (16-byte loads, a tile ahead in
+//                   registers) to fp16 in the 128-byte-swizzled layout, K and V
+//                   alike, two stages each
+//   warp 12         one thread issues tcgen05.mma kind::f16: S = Q K^T from
+//                   shared memory, O += W V with W from tensor memory (it
+//                   lies where S was), the two row tiles in turn, so that one
+//                   tile's softmax runs under the other's products
+// Every mbarrier wait is bounded; a CTA that gives up sets the device error
+// word, waits for its products and frees its tensor memory.
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "serving.cuh"
+#include "sm100.cuh"
+
+namespace hbl {
+namespace {
+
+using namespace sm100;
+
+constexpr int kRowsM = 128;               // rows of one tile
+constexpr int kRows = 2 * kRowsM;         // rows of a CTA
+constexpr int kKeys = 128;                // tokens of a tile
+constexpr int kThreads = 13 * 32;
+constexpr int kMeta = 4;                  // slots of page scales
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kS = 0, kO = 256;      // tensor memory columns: S0 and S1 (W in their place), O0 and O1
+constexpr float kTop = 11.0f;             // log2 of the weight at the reference maximum
+constexpr float kSlack = 4.0f;            // what the maximum may grow by before the reference follows
+constexpr float kLog2e = 1.4426950408889634f;
+
+// kind::f16, D f32, A and B fp16, M = 128: scores (both K-major, N = 128 tokens), outputs (B MN-major, N = D)
+constexpr uint32_t kIdescS = (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+template <int D>
+constexpr uint32_t kIdescO = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((128u >> 4) << 24);
+
+template <int D>
+struct Shape {
+  static constexpr int kHalves = D / 64;             // blocks of 64 values: 128 rows of 128 bytes
+  static constexpr int kBlock = 128 * 128;
+  static constexpr int kTile = kHalves * kBlock;     // a Q, K or V tile in fp16
+  static constexpr size_t kSmem = 1024 + 6 * (size_t)kTile + kMeta * 8 * 16 + 256;
+  static constexpr int kVectors = D / 16;            // 16-byte code vectors per converting thread and tile
+};
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate));
+}
+
+// sixteen columns of this thread's lane; the registers hold them after landed()
+__device__ __forceinline__ void tmem_ld16(uint32_t at, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(at));
+}
+__device__ __forceinline__ void landed(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+// (a0, a1) * m + c
+__device__ __forceinline__ void fma2(float& a0, float& a1, float m, float c) {
+  asm("{\n\t.reg .b64 A, M, C;\n\t"
+      "mov.b64 A, {%0, %1};\n\tmov.b64 M, {%2, %2};\n\tmov.b64 C, {%3, %3};\n\t"
+      "fma.rn.f32x2 A, A, M, C;\n\tmov.b64 {%0, %1}, A;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(m), "f"(c));
+}
+__device__ __forceinline__ void add2(float& s0, float& s1, float a0, float a1) {
+  asm("{\n\t.reg .b64 A, S;\n\t"
+      "mov.b64 A, {%2, %3};\n\tmov.b64 S, {%0, %1};\n\t"
+      "add.rn.f32x2 S, S, A;\n\tmov.b64 {%0, %1}, S;\n\t}"
+      : "+f"(s0), "+f"(s1)
+      : "f"(a0), "f"(a1));
+}
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// place of 16 bytes (eight fp16 values) of row t in a block of 64 values
+__device__ __forceinline__ uint32_t swizzled(int t, int piece) { return (uint32_t)(t * 128 + ((piece ^ (t & 7)) << 4)); }
+
+// The CTA's item: which request, its rows, and where they stand.
+struct Item {
+  int b, row0, n;        // request, its first row of the batch, its rows
+  int first;             // first of the CTA's rows, in (row, head of the group) order
+  int keys, pos0;        // tokens that the table can hold; position of the request's first row
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const KvAttentionArgs a, int* err) {
+  using S = Shape<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  const uint32_t q_at = smem_u32(base), k_at = q_at + 2 * S::kTile, v_at = k_at + 2 * S::kTile;
+  const uint32_t meta_at = v_at + 2 * S::kTile;
+  float4* meta = reinterpret_cast<float4*>(base + 6 * S::kTile);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(base + 6 * S::kTile + kMeta * 8 * 16);
+  uint64_t *kfull = bars, *kempty = bars + 2, *vfull = bars + 4, *vempty = bars + 6, *sfull = bars + 8,
+           *pready = bars + 10, *odone = bars + 12, *mready = bars + 14, *qready = bars + 18, *drain = bars + 19;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 20);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  __shared__ Item item;
+  __shared__ int64_t warp_sums[kThreads / 32];
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = a.Hq / a.Hkv;
+  const int h = blockIdx.x % a.Hkv;
+  const int64_t rank = blockIdx.x / a.Hkv;
+
+  // ---- which 256 rows: the request whose row tiles hold this CTA's rank
+  {
+    const int per = (a.B + kThreads - 1) / kThreads, b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+    auto rows_of = [&](int b, int& row0) {
+      row0 = min(max(a.row_start[b], 0), (int)a.T);
+      return min(max(a.row_start[b + 1], row0), (int)a.T) - row0;
+    };
+    if (tid == 0) item.b = -1;
+    int64_t s = 0;
+    int row0;
+    for (int b = b0; b < b1; ++b) s += ((int64_t)rows_of(b, row0) * g + kRows - 1) / kRows;
+    int64_t inc = s;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t u = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += u;
+    }
+    if (lane == 31) warp_sums[warp] = inc;
+    __syncthreads();
+    int64_t at = inc - s;
+    for (int w = 0; w < warp; ++w) at += warp_sums[w];
+    if (rank >= at && rank < at + s) {
+      for (int b = b0; b < b1; ++b) {
+        const int n = rows_of(b, row0);
+        const int tiles = (int)(((int64_t)n * g + kRows - 1) / kRows);
+        if (rank < at + tiles) {
+          const int total = max(a.total[b], 0);
+          const int64_t limit = a.width * a.block;
+          // the last rows see most tokens: they go first
+          item = {b, row0, n, (int)(tiles - 1 - (rank - at)) * kRows, limit < total ? (int)limit : total, total - n};
+          break;
+        }
+        at += tiles;
+      }
+    }
+    __syncthreads();
+  }
+  const Item it = item;
+  if (it.b < 0) return;
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&kfull[i], 4);
+      mbar_init(&kempty[i], 1);
+      mbar_init(&vfull[i], 4);
+      mbar_init(&vempty[i], 1);
+      mbar_init(&sfull[i], 1);
+      mbar_init(&pready[i], 4);
+      mbar_init(&odone[i], 1);
+    }
+    for (int i = 0; i < kMeta; ++i) mbar_init(&mready[i], 4);
+    mbar_init(qready, 8);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == 12) tmem_alloc(tmem_slot, kTmemCols);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  // tokens that the last row of a tile sees, in tiles
+  const int rows = it.n * g;
+  auto tiles_of = [&](int mt) {
+    const int last = min(it.first + (mt + 1) * kRowsM, rows) - 1;
+    if (last < it.first + mt * kRowsM) return 0;
+    const int sees = min(it.pos0 + last / g + 1, it.keys);
+    return sees > 0 ? (sees - 1) / kKeys + 1 : 0;
+  };
+  const int n0 = tiles_of(0), n1 = tiles_of(1), n = max(n0, n1);
+
+  if (warp < 8) {
+    // ------------------------------------------------ softmax: one row per thread
+    const int mt = warp >> 2, mine = mt ? n1 : n0;
+    const int row = it.first + mt * kRowsM + (warp & 3) * 32 + lane;
+    const bool live = row < rows;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_tm = tmem + kS + mt * 128 + lanes, o_tm = tmem + kO + mt * D + lanes;
+    const float scale = a.scale ? *a.scale : rsqrtf((float)D);
+    float q_scale, q_sum = 0.0f;
+    {
+      // the row into fp16, its largest value in [2^10, 2^11)
+      const uint16_t* q = reinterpret_cast<const uint16_t*>(a.q) +
+                          (live ? (int64_t)(it.row0 + row / g) * a.q_stride + ((int64_t)h * g + row % g) * D : 0);
+      const uint4* from = reinterpret_cast<const uint4*>(q);
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        const uint4 v = live ? __ldg(from + i) : make_uint4(0, 0, 0, 0);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          asm("max.bf16x2 %0, %0, %1;" : "+r"(top) : "r"(w[e] & 0x7FFF7FFFu));  // a NaN gives way to a number
+      }
+      const float amax = fmaxf(__uint_as_float(top << 16), __uint_as_float(top & 0xFFFF0000u));
+      const int e2 = max((int)(__float_as_uint(amax) >> 23) - 127, -100);
+      const float up = __uint_as_float((uint32_t)(127 + 10 - e2) << 23), down = __uint_as_float((uint32_t)(127 - 10 + e2) << 23);
+      const float sign = scale < 0.0f ? -up : up;
+      q_scale = fabsf(scale) * kLog2e * down;
+      const int t = (warp & 3) * 32 + lane;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        const uint4 v = live ? __ldg(from + i) : make_uint4(0, 0, 0, 0);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          o[e] = pack2(__uint_as_float(w[e] << 16) * sign, __uint_as_float(w[e] & 0xFFFF0000u) * sign);
+          const __half2 hv = *reinterpret_cast<const __half2*>(&o[e]);
+          q_sum += __low2float(hv) + __high2float(hv);
+        }
+        sts128(q_at + mt * S::kTile + (i / 8) * S::kBlock + swizzled(t, i % 8), o[0], o[1], o[2], o[3]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(qready);
+    }
+
+    float ref = -INFINITY, l = 0.0f, ws = 0.0f;
+    // tokens that the row sees; rows that are none see all (their scores are 0)
+    const int sees = live ? min(it.pos0 + row / g + 1, it.keys) : INT32_MAX;
+    bool ok = true;
+    for (int i = 0; i < mine; ++i) {
+      if (!wait_bounded_warp(&mready[i % kMeta], (uint32_t)(i / kMeta) & 1u, abort_flag, err) ||
+          !wait_bounded_warp(&sfull[mt], (uint32_t)i & 1u, abort_flag, err)) {
+        ok = false;
+        break;
+      }
+      __syncwarp();
+      fence_after();
+      const int lim = sees - i * kKeys;
+      const bool masked = __any_sync(0xffffffffu, lim < kKeys);
+      const uint32_t pages = meta_at + (i % kMeta) * 128;
+      uint32_t w[8][8];
+      float top, sum, all;
+      // one pass over the row's scores: weights under the reference (-inf: 0 in its place), their sums, the maximum
+      auto pass = [&](auto with_mask) {
+        const float off = kTop - (ref == -INFINITY ? 0.0f : ref);
+        top = -INFINITY;
+        sum = all = 0.0f;
+        uint32_t s[2][16];
+        tmem_ld16(s_tm, s[0]);
+#pragma unroll
+        for (int grp = 0; grp < 8; ++grp) {
+          landed(s[grp & 1]);
+          if (grp < 7) tmem_ld16(s_tm + 16 * (grp + 1), s[(grp + 1) & 1]);
+          float v[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(s[grp & 1][e]);
+          // scale of the keys, log2 of the values' scale, its inverse, values not all zero
+          const uint4 p = lds128(pages + grp * 16);
+          const float f = q_scale * __uint_as_float(p.x), c = fmaf(q_sum, f, __uint_as_float(p.y)), f2 = 2.0f * f;
+          if constexpr (!decltype(with_mask)::value) {
+            float m = fmaxf(v[0], v[1]);
+#pragma unroll
+            for (int e = 2; e < 16; e += 2) m = fmaxf(m, fmaxf(v[e], v[e + 1]));
+            top = fmaxf(top, fmaf(m, f2, c));
+          }
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) fma2(v[e], v[e + 1], f2, c + off);
+          if constexpr (decltype(with_mask)::value) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              if (grp * 16 + e >= lim) v[e] = -INFINITY;
+              top = fmaxf(top, v[e] - off);
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = ex2(v[e]);
+          float s0 = v[0], s1 = v[1];
+#pragma unroll
+          for (int e = 2; e < 16; e += 2) add2(s0, s1, v[e], v[e + 1]);
+          s0 += s1;
+          sum = fmaf(s0, __uint_as_float(p.z), sum);
+          // a page whose values are all zero takes part in the sum alone
+          const bool some = p.w != 0;
+          all += some ? s0 : 0.0f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w[grp][e] = some ? pack2(v[2 * e], v[2 * e + 1]) : 0u;
+        }
+      };
+      auto run = [&] {
+        if (masked)
+          pass(std::true_type());
+        else
+          pass(std::false_type());
+      };
+      run();
+      const bool follow = top > ref + kSlack || (ref == -INFINITY && top > -INFINITY);
+      if (__any_sync(0xffffffffu, follow)) {
+        const float next = follow ? top : ref;
+        const float grow = ref == -INFINITY ? 0.0f : ex2(ref - next);
+        if (i > 0) {
+          if (!wait_bounded_warp(&odone[mt], (uint32_t)(i - 1) & 1u, abort_flag, err)) {
+            ok = false;
+            break;
+          }
+          __syncwarp();
+          fence_after();
+          const float by = follow ? grow : 1.0f;
+#pragma unroll 1
+          for (int x = 0; x < D; x += 16) {
+            uint32_t r[16];
+            tmem_ld16(o_tm + x, r);
+            landed(r);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * by);
+            tmem_st16(o_tm + x, r);
+          }
+        }
+        if (follow) {
+          l *= grow;
+          ws *= grow;
+          ref = next;
+        }
+        run();
+      }
+      l += sum;
+      ws += all;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        uint32_t r[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) r[e] = w[2 * x + e / 8][e % 8];
+        tmem_st16(s_tm + 16 * x, r);
+      }
+      tmem_wait_st();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&pready[mt]);
+    }
+    // ---- o = (2 O + sum of the weights) / l
+    if (ok && mine > 0) ok = wait_bounded_warp(&odone[mt], (uint32_t)(mine - 1) & 1u, abort_flag, err);
+    ok = __all_sync(0xffffffffu, ok);
+    fence_after();
+    if (ok) {
+      const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
+      const int64_t at = live ? ((int64_t)(it.row0 + row / g) * a.Hq + (int64_t)h * g + row % g) * D : 0;
+#pragma unroll 1
+      for (int x = 0; x < D; x += 16) {
+        uint32_t r[16];
+        float v[16];
+        if (mine > 0) {
+          tmem_ld16(o_tm + x, r);
+          landed(r);
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = mine > 0 ? fmaf(2.0f, __uint_as_float(r[e]), ws) * inv : 0.0f;
+        if (live && a.o_bf16) {
+          uint32_t p[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(p[e]) : "f"(v[2 * e + 1]), "f"(v[2 * e]));
+          uint4* to = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.o) + at + x);
+          to[0] = make_uint4(p[0], p[1], p[2], p[3]);
+          to[1] = make_uint4(p[4], p[5], p[6], p[7]);
+        } else if (live) {
+          float4* to = reinterpret_cast<float4*>(reinterpret_cast<float*>(a.o) + at + x);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) to[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+        }
+        __syncwarp();
+      }
+    }
+  } else if (warp < 12) {
+    // ------------------------------------------------ codes to fp16, 32 tokens of a tile per warp
+    const int cw = warp - 8;
+    constexpr int kPerHalf = S::kHalves;   // neighbouring vectors alternate between the halves of a token's row
+    const int32_t* pages = a.table + (int64_t)it.b * a.width;
+    const int block_shift = 31 - __clz(a.block);
+    const int L = (1 << a.bits) - 1;
+    const uint32_t minus = 0xE400E400u | ((uint32_t)(1 << (a.bits - 1)) * 0x10001u);  // -(1024 + z), twice
+    auto page_of = [&](int i, int grp) {
+      const int tok = i * kKeys + cw * 32 + grp * 16;
+      const int v = i < n && tok < it.keys ? pages[tok >> block_shift] : -1;
+      return v >= 0 && v < a.num_blocks ? v : -1;
+    };
+    const int my_tok = lane >> 2, my_piece = lane & 3;
+    auto load = [&](const uint8_t* codes, int i, const int (&id)[2], uint4 (&v)[S::kVectors]) {
+#pragma unroll
+      for (int j = 0; j < S::kVectors; ++j) {
+        const int half = j % kPerHalf, tok = (j / kPerHalf) * 8 + my_tok;   // tok < 32
+        const int page = id[(j / kPerHalf) >> 1];
+        const int64_t from =
+            (((int64_t)page * a.Hkv + h) * a.block + ((i * kKeys + cw * 32 + tok) & (a.block - 1))) * D + half * 64 + my_piece * 16;
+        v[j] = page >= 0 ? *reinterpret_cast<const uint4*>(codes + from) : make_uint4(0, 0, 0, 0);
+      }
+    };
+    auto convert = [&](uint32_t tile, const int (&id)[2], const uint4 (&v)[S::kVectors]) {
+#pragma unroll
+      for (int j = 0; j < S::kVectors; ++j) {
+        const int half = j % kPerHalf, tok = cw * 32 + (j / kPerHalf) * 8 + my_tok;
+        const bool there = id[(j / kPerHalf) >> 1] >= 0;
+        const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+        uint32_t o[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          asm("add.rn.f16x2 %0, %1, %2;" : "=r"(o[2 * e]) : "r"(__byte_perm(w[e], 0x64646464u, 0x4140u)), "r"(minus));
+          asm("add.rn.f16x2 %0, %1, %2;" : "=r"(o[2 * e + 1]) : "r"(__byte_perm(w[e], 0x64646464u, 0x4342u)), "r"(minus));
+        }
+        if (!there) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] = 0u;
+        }
+        const uint32_t at = tile + half * S::kBlock;
+        sts128(at + swizzled(tok, 2 * my_piece), o[0], o[1], o[2], o[3]);
+        sts128(at + swizzled(tok, 2 * my_piece + 1), o[4], o[5], o[6], o[7]);
+      }
+    };
+    int id[2], next[2];
+    uint4 kv[S::kVectors], vv[S::kVectors];
+    float ks = 0.0f, vs = 0.0f;  // scales of the page of the group that this lane (0 or 1) writes down
+#pragma unroll
+    for (int e = 0; e < 2; ++e) id[e] = page_of(0, e), next[e] = page_of(1, e);
+    load(a.k_codes, 0, id, kv);
+    load(a.v_codes, 0, id, vv);
+    auto scales = [&](const int (&of)[2]) {
+      const int page = lane == 0 ? of[0] : of[1];
+      if (lane < 2 && page >= 0) {
+        ks = a.k_scales[(int64_t)page * a.Hkv + h];
+        vs = a.v_scales[(int64_t)page * a.Hkv + h];
+      }
+    };
+    scales(id);
+    for (int i = 0; i < n; ++i) {
+      const int st = i & 1;
+      const uint32_t reuse = ((uint32_t)(i >> 1) & 1u) ^ 1u;
+      if (!wait_bounded_warp(&kempty[st], reuse, abort_flag, err)) break;
+      if (lane < 2) {
+        const bool there = (lane == 0 ? id[0] : id[1]) >= 0;
+        const float vu = __fdiv_rn(vs, (float)L);
+        const bool some = vu >= 1e-30f;
+        const float lu = __log2f(some ? vu : 1e-30f);
+        meta[(i % kMeta) * 8 + cw * 2 + lane] =
+            there ? make_float4(__fdiv_rn(ks, (float)L), lu, ex2(-lu), some ? 1.0f : 0.0f)
+                  : make_float4(0.0f, -INFINITY, 0.0f, 0.0f);
+      }
+      convert(k_at + st * S::kTile, id, kv);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&mready[i % kMeta]);
+        mbar_arrive(&kfull[st]);
+      }
+      if (i + 1 < n) {
+        load(a.k_codes, i + 1, next, kv);
+        scales(next);
+      }
+      if (!wait_bounded_warp(&vempty[st], reuse, abort_flag, err)) break;
+      convert(v_at + st * S::kTile, id, vv);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&vfull[st]);
+      if (i + 1 < n) load(a.v_codes, i + 1, next, vv);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) id[e] = next[e], next[e] = page_of(i + 2, e);
+    }
+  } else if (lane == 0) {
+    // ------------------------------------------------ products
+    auto scores = [&](int mt, int st) {
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const uint32_t in = (k / 4) * S::kBlock;
+        mma_ss(tmem + kS + mt * 128, sdesc_k_sw128(q_at + mt * S::kTile + in) + (uint64_t)(2 * (k % 4)),
+               sdesc_k_sw128(k_at + st * S::kTile + in) + (uint64_t)(2 * (k % 4)), kIdescS, k > 0 ? 1u : 0u);
+      }
+      umma_commit(&sfull[mt]);
+    };
+    bool ok = n == 0 || (wait_bounded(qready, 0, abort_flag, err) && wait_bounded(&kfull[0], 0, abort_flag, err));
+    if (ok && n > 0) {
+      fence_after();
+      if (n0 > 0) scores(0, 0);
+      if (n1 > 0) scores(1, 0);
+      umma_commit(&kempty[0]);
+    }
+    for (int i = 0; i < n && ok; ++i) {
+      const int st = i & 1, nst = st ^ 1;
+      if (!wait_bounded(&vfull[st], (uint32_t)(i >> 1) & 1u, abort_flag, err)) break;
+      if (i + 1 < n && !wait_bounded(&kfull[nst], (uint32_t)((i + 1) >> 1) & 1u, abort_flag, err)) break;
+      for (int mt = 0; mt < 2; ++mt) {
+        const int mine = mt ? n1 : n0;
+        if (i < mine) {
+          if (!wait_bounded(&pready[mt], (uint32_t)i & 1u, abort_flag, err)) {
+            ok = false;
+            break;
+          }
+          fence_after();
+          const uint64_t v0 = sdesc_mn_sw128(v_at + st * S::kTile, S::kBlock);
+#pragma unroll
+          for (int k = 0; k < kKeys / 16; ++k)
+            mma_ts(tmem + kO + mt * D, tmem + kS + mt * 128 + 8u * k, v0 + (uint64_t)(128 * k), kIdescO<D>,
+                   (i | k) != 0 ? 1u : 0u);
+          umma_commit(&odone[mt]);
+        }
+        if (i + 1 < mine) scores(mt, nst);
+      }
+      if (!ok) break;
+      umma_commit(&vempty[st]);
+      if (i + 1 < n) umma_commit(&kempty[nst]);
+    }
+    // all products issued are complete before tensor memory is freed
+    umma_commit(drain);
+    drain_wait(drain, 0, err);
+  }
+
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == 12) tmem_dealloc(tmem, kTmemCols);
+}
+
+template <int D>
+cudaError_t launch(const KvAttentionArgs& a, cudaStream_t stream) {
+  int* err = device_error_word();
+  if (!err) return cudaErrorInvalidValue;
+  static std::atomic<bool> done[sm100_host::kMaxDevices];
+  cudaError_t e = sm100_host::ensure_smem(kv_attention_prompt_kernel<D>, (int)Shape<D>::kSmem, done);
+  if (e != cudaSuccess) return e;
+  // a CTA for each row tile that the batch can have, whatever its rows' split over the requests
+  const int64_t tiles = (a.T * (a.Hq / a.Hkv) + kRows - 1) / kRows + a.B;
+  kv_attention_prompt_kernel<D><<<(unsigned)(tiles * a.Hkv), kThreads, Shape<D>::kSmem, stream>>>(a, err);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+bool kv_attention_prompt_supports(const KvAttentionArgs& a) {
+  return a.q_bf16 && (a.D == 64 || a.D == 128) && a.T * (a.Hq / a.Hkv) >= kPromptRows * (int64_t)a.B &&
+         (a.T * (a.Hq / a.Hkv) / kRows + 1 + a.B) * a.Hkv <= INT32_MAX;
+}
+
+cudaError_t launch_kv_attention_prompt(const KvAttentionArgs& a, cudaStream_t stream) {
+  return a.D == 64 ? launch<64>(a, stream) : launch<128>(a, stream);
+}
+
+}  // namespace hbl

@@ -62,6 +62,11 @@ struct KvAttentionArgs {
 };
 size_t kv_attention_workspace(int64_t T, int Hq, int Hkv, int D, int B);
 cudaError_t launch_kv_attention(const KvAttentionArgs& a, cudaStream_t stream);
+// The same with 256-row tiles on tcgen05 (kv_attention_prompt.cu), for bf16
+// queries from kPromptRows rows per request and cached head on average.
+constexpr int64_t kPromptRows = 64;
+bool kv_attention_prompt_supports(const KvAttentionArgs& a);
+cudaError_t launch_kv_attention_prompt(const KvAttentionArgs& a, cudaStream_t stream);
 
 cudaError_t launch_add_rms_quant(const void* x, const void* residual, bool bf16, int64_t M, int64_t K,
                                  const float* gain, int bits, void* h, int8_t* codes, float* scales,
