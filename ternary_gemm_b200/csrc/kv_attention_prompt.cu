@@ -8,9 +8,11 @@
 //   w_j = exp(s_j) u_v(j),   o = sum_j w_j (2 v'_j + 1) / sum_j w_j / u_v(j)
 //
 // and the weights are held on a scale where a row's largest lies in
-// [2^11, 2^15]: the scale follows the running maximum only when that grew by
-// more than four powers of two, so the accumulator in tensor memory is seldom
-// rescaled, and fp16 keeps 11 bits of all weights down to 2^-25 of the largest.
+// [2^7, 2^15]: the scale follows the running maximum only when that grew by
+// more than eight powers of two, so the accumulator in tensor memory is seldom
+// rescaled (with four, some warp of the CTA had to in every other tile, and the
+// whole took 571 us instead of 330 at 2048 rows over 8192 tokens), and fp16
+// keeps 11 bits of all weights down to 2^-21 of the largest at the least.
 //
 // Rows are many, so this is a matter of the tensor cores: a CTA takes 256 rows
 // of one cached head (two tiles of 128, query heads of the group times the
@@ -47,8 +49,8 @@ constexpr int kThreads = 13 * 32;
 constexpr int kMeta = 4;                  // slots of page scales
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kS = 0, kO = 256;      // tensor memory columns: S0 and S1 (W in their place), O0 and O1
-constexpr float kTop = 11.0f;             // log2 of the weight at the reference maximum
-constexpr float kSlack = 4.0f;            // what the maximum may grow by before the reference follows
+constexpr float kTop = 7.0f;              // log2 of the weight at the reference maximum
+constexpr float kSlack = 8.0f;            // what the maximum may grow by before the reference follows
 constexpr float kLog2e = 1.4426950408889634f;
 
 // kind::f16, D f32, A and B fp16, M = 128: scores (both K-major, N = 128 tokens), outputs (B MN-major, N = D)

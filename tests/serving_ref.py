@@ -131,11 +131,11 @@ def attention_tolerance(o, mass, reach, crest, keys, q_f32, o_f32):
     float); the weights' rounding to fp16, 2^-11 (float q: two parts, 2^-22); a score's error moves its weight and the
     sum: twice 2^-18 reach (22-bit products, at most 32 float accumulation steps of 2^-23 each, which truncate) and
     2^-20 for the exponential and the scaling; and float accumulation over the keys in steps of 16.  A weight times its
-    block's gamma is held on a scale where the row's largest lies in [2^11, 2^15]: what is below fp16's normal numbers
-    there is off by half its smallest step, 2^-25, at most 2^-36 of crest for a key; weights that underflow float,
+    block's gamma is held on a scale where the row's largest lies in [2^7, 2^15]: what is below fp16's normal numbers
+    there is off by half its smallest step, 2^-25, at most 2^-32 of crest for a key; weights that underflow float,
     2^-126."""
     weights = (2.0 ** -22 if q_f32 else 2.0 ** -11) + 2 * (2.0 ** -18 * reach + 2.0 ** -20) + (keys / 16 + 8) * 2.0 ** -23
-    return (2.0 ** -24 if o_f32 else 2.0 ** -8) * np.abs(o) + weights * mass + keys * (2.0 ** -36 * crest + 2.0 ** -126)
+    return (2.0 ** -24 if o_f32 else 2.0 ** -8) * np.abs(o) + weights * mass + keys * (2.0 ** -32 * crest + 2.0 ** -126)
 
 
 # ------------------------------------------------------------------ residual, RMSNorm, quantizer
