@@ -22,10 +22,10 @@
 //   warps 8-11      codes from the pages (16-byte loads, a tile ahead in
 //                   registers) to fp16 in the 128-byte-swizzled layout, K and V
 //                   alike, two stages each
-//   warp 12         one thread issues tcgen05.mma kind::f16: S = Q K^T from
-//                   shared memory, O += W V with W from tensor memory (it
-//                   lies where S was), the two row tiles in turn, so that one
-//                   tile's softmax runs under the other's products
+//   warp 12         issues tcgen05.mma kind::f16: S = Q K^T from shared memory,
+//                   O += W V with W from tensor memory (it lies where S was),
+//                   the two row tiles in turn, so that one tile's softmax runs
+//                   under the other's products
 // Every mbarrier wait is bounded; a CTA that gives up sets the device error
 // word, waits for its products and frees its tensor memory.
 #include <cstdint>
@@ -67,19 +67,31 @@ struct Shape {
   static constexpr int kVectors = D / 16;            // 16-byte code vectors per converting thread and tile
 };
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// Descriptors differ in their low words alone (the address, in 16-byte units).
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t a_high, uint32_t b, uint32_t b_high, uint32_t idesc,
+                                       uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
+      "{\n\t.reg .pred p;\n\t.reg .b64 A, B;\n\t"
+      "mov.b64 A, {%1, %2};\n\tmov.b64 B, {%3, %4};\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], A, B, %5, p;\n\t}\n" ::"r"(d),
+      "r"(a), "r"(a_high), "r"(b), "r"(b_high), "r"(idesc), "r"(accumulate));
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t b_high, uint32_t idesc,
+                                       uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate));
+      "{\n\t.reg .pred p;\n\t.reg .b64 B;\n\t"
+      "mov.b64 B, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], B, %4, p;\n\t}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(b_high), "r"(idesc), "r"(accumulate));
+}
+
+// true in one lane of the warp, the same one every time
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 
 // sixteen columns of this thread's lane; the registers hold them after landed()
@@ -142,6 +154,18 @@ __device__ __forceinline__ void sts128(uint32_t at, uint32_t a, uint32_t b, uint
 // place of 16 bytes (eight fp16 values) of row t in a block of 64 values
 __device__ __forceinline__ uint32_t swizzled(int t, int piece) { return (uint32_t)(t * 128 + ((piece ^ (t & 7)) << 4)); }
 
+// What a row's scores of sixteen tokens of one page are to be multiplied by and
+// added to, the inverse of the values' scale, and whether any value is not 0.
+struct Page {
+  float f2, c, inv;
+  bool some;
+};
+__device__ __forceinline__ Page page_at(uint32_t pages, int grp, float q_scale, float q_sum) {
+  const uint4 p = lds128(pages + grp * 16);
+  const float f = q_scale * __uint_as_float(p.x);
+  return {2.0f * f, fmaf(q_sum, f, __uint_as_float(p.y)), __uint_as_float(p.z), p.w != 0};
+}
+
 // The CTA's item: which request, its rows, and where they stand.
 struct Item {
   int b, row0, n;        // request, its first row of the batch, its rows
@@ -159,13 +183,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
   float4* meta = reinterpret_cast<float4*>(base + 6 * S::kTile);
   uint64_t* bars = reinterpret_cast<uint64_t*>(base + 6 * S::kTile + kMeta * 8 * 16);
   uint64_t *kfull = bars, *kempty = bars + 2, *vfull = bars + 4, *vempty = bars + 6, *sfull = bars + 8,
-           *pready = bars + 10, *odone = bars + 12, *mready = bars + 14, *qready = bars + 18, *drain = bars + 19;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 20);
+           *pready = bars + 10, *odone = bars + 14, *mready = bars + 16, *qready = bars + 20, *drain = bars + 21,
+           *ofinal = bars + 22;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 24);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   __shared__ Item item;
   __shared__ int64_t warp_sums[kThreads / 32];
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int g = a.Hq / a.Hkv;
   const int h = blockIdx.x % a.Hkv;
   const int64_t rank = blockIdx.x / a.Hkv;
@@ -217,8 +242,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
       mbar_init(&vfull[i], 4);
       mbar_init(&vempty[i], 1);
       mbar_init(&sfull[i], 1);
-      mbar_init(&pready[i], 4);
+      mbar_init(&pready[2 * i], 4);
+      mbar_init(&pready[2 * i + 1], 4);
       mbar_init(&odone[i], 1);
+      mbar_init(&ofinal[i], 1);
     }
     for (int i = 0; i < kMeta; ++i) mbar_init(&mready[i], 4);
     mbar_init(qready, 8);
@@ -231,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
   // tokens that the last row of a tile sees, in tiles
   const int rows = it.n * g;
@@ -305,106 +332,109 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
       const int lim = sees - i * kKeys;
       const bool masked = __any_sync(0xffffffffu, lim < kKeys);
       const uint32_t pages = meta_at + (i % kMeta) * 128;
-      uint32_t w[8][8];
-      float top, sum, all;
-      // one pass over the row's scores: weights under the reference (-inf: 0 in its place), their sums, the maximum
-      auto pass = [&](auto with_mask) {
-        const float off = kTop - (ref == -INFINITY ? 0.0f : ref);
-        top = -INFINITY;
-        sum = all = 0.0f;
-        uint32_t s[2][16];
-        tmem_ld16(s_tm, s[0]);
+      // the tile in two halves, so that the products of the first begin while the second is worked on
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        uint32_t w[4][8];
+        float top, sum, all;
+        // one reading of the half's scores: weights under the reference (-inf: 0 in its place), their sums, the maximum
+        auto pass = [&](auto with_mask) {
+          const float off = kTop - (ref == -INFINITY ? 0.0f : ref);
+          top = -INFINITY;
+          sum = all = 0.0f;
+          uint32_t s[2][16];
+          tmem_ld16(s_tm + 64 * half, s[0]);
 #pragma unroll
-        for (int grp = 0; grp < 8; ++grp) {
-          landed(s[grp & 1]);
-          if (grp < 7) tmem_ld16(s_tm + 16 * (grp + 1), s[(grp + 1) & 1]);
-          float v[16];
+          for (int grp = 0; grp < 4; ++grp) {
+            landed(s[grp & 1]);
+            if (grp < 3) tmem_ld16(s_tm + 64 * half + 16 * (grp + 1), s[(grp + 1) & 1]);
+            float v[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(s[grp & 1][e]);
-          // scale of the keys, log2 of the values' scale, its inverse, values not all zero
-          const uint4 p = lds128(pages + grp * 16);
-          const float f = q_scale * __uint_as_float(p.x), c = fmaf(q_sum, f, __uint_as_float(p.y)), f2 = 2.0f * f;
-          if constexpr (!decltype(with_mask)::value) {
-            float m = fmaxf(v[0], v[1]);
+            for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(s[grp & 1][e]);
+            const Page p = page_at(pages, 4 * half + grp, q_scale, q_sum);
+            if constexpr (!decltype(with_mask)::value) {
+              float m0 = v[0], m1 = v[1];
 #pragma unroll
-            for (int e = 2; e < 16; e += 2) m = fmaxf(m, fmaxf(v[e], v[e + 1]));
-            top = fmaxf(top, fmaf(m, f2, c));
+              for (int e = 2; e < 16; e += 2) m0 = fmaxf(m0, v[e]), m1 = fmaxf(m1, v[e + 1]);
+              top = fmaxf(top, fmaf(fmaxf(m0, m1), p.f2, p.c));
+            }
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) fma2(v[e], v[e + 1], p.f2, p.c + off);
+            if constexpr (decltype(with_mask)::value) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                if (64 * half + 16 * grp + e >= lim) v[e] = -INFINITY;
+                top = fmaxf(top, v[e] - off);
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] = ex2(v[e]);
+            float s0 = v[0], s1 = v[1];
+#pragma unroll
+            for (int e = 2; e < 16; e += 2) add2(s0, s1, v[e], v[e + 1]);
+            s0 += s1;
+            sum = fmaf(s0, p.inv, sum);
+            // a page whose values are all zero takes part in the sum alone
+            all += p.some ? s0 : 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[grp][e] = p.some ? pack2(v[2 * e], v[2 * e + 1]) : 0u;
           }
+        };
+        auto run = [&] {
+          if (masked)
+            pass(std::true_type());
+          else
+            pass(std::false_type());
+        };
+        run();
+        const bool follow = top > ref + kSlack || (ref == -INFINITY && top > -INFINITY);
+        if (__any_sync(0xffffffffu, follow)) {
+          const float next = follow ? top : ref;
+          const float grow = ref == -INFINITY ? 0.0f : ex2(ref - next);
+          if (i + half > 0) {
+            // the products up to the half before this one (the one before that is known to have ended)
+            if (!wait_bounded_warp(&odone[mt], (uint32_t)(half ^ 1), abort_flag, err)) {
+              ok = false;
+              break;
+            }
+            __syncwarp();
+            fence_after();
+            const float by = follow ? grow : 1.0f;
+#pragma unroll 1
+            for (int x = 0; x < D; x += 16) {
+              uint32_t r[16];
+              tmem_ld16(o_tm + x, r);
+              landed(r);
 #pragma unroll
-          for (int e = 0; e < 16; e += 2) fma2(v[e], v[e + 1], f2, c + off);
-          if constexpr (decltype(with_mask)::value) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              if (grp * 16 + e >= lim) v[e] = -INFINITY;
-              top = fmaxf(top, v[e] - off);
+              for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * by);
+              tmem_st16(o_tm + x, r);
             }
           }
-#pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = ex2(v[e]);
-          float s0 = v[0], s1 = v[1];
-#pragma unroll
-          for (int e = 2; e < 16; e += 2) add2(s0, s1, v[e], v[e + 1]);
-          s0 += s1;
-          sum = fmaf(s0, __uint_as_float(p.z), sum);
-          // a page whose values are all zero takes part in the sum alone
-          const bool some = p.w != 0;
-          all += some ? s0 : 0.0f;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) w[grp][e] = some ? pack2(v[2 * e], v[2 * e + 1]) : 0u;
-        }
-      };
-      auto run = [&] {
-        if (masked)
-          pass(std::true_type());
-        else
-          pass(std::false_type());
-      };
-      run();
-      const bool follow = top > ref + kSlack || (ref == -INFINITY && top > -INFINITY);
-      if (__any_sync(0xffffffffu, follow)) {
-        const float next = follow ? top : ref;
-        const float grow = ref == -INFINITY ? 0.0f : ex2(ref - next);
-        if (i > 0) {
-          if (!wait_bounded_warp(&odone[mt], (uint32_t)(i - 1) & 1u, abort_flag, err)) {
-            ok = false;
-            break;
+          if (follow) {
+            l *= grow;
+            ws *= grow;
+            ref = next;
           }
-          __syncwarp();
-          fence_after();
-          const float by = follow ? grow : 1.0f;
-#pragma unroll 1
-          for (int x = 0; x < D; x += 16) {
-            uint32_t r[16];
-            tmem_ld16(o_tm + x, r);
-            landed(r);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * by);
-            tmem_st16(o_tm + x, r);
-          }
+          run();
         }
-        if (follow) {
-          l *= grow;
-          ws *= grow;
-          ref = next;
+        l += sum;
+        ws += all;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          uint32_t r[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) r[e] = w[2 * x + e / 8][e % 8];
+          tmem_st16(s_tm + 32 * half + 16 * x, r);
         }
-        run();
+        tmem_wait_st();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pready[2 * mt + half]);
       }
-      l += sum;
-      ws += all;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        uint32_t r[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) r[e] = w[2 * x + e / 8][e % 8];
-        tmem_st16(s_tm + 16 * x, r);
-      }
-      tmem_wait_st();
-      fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&pready[mt]);
+      if (!ok) break;
     }
     // ---- o = (2 O + sum of the weights) / l
-    if (ok && mine > 0) ok = wait_bounded_warp(&odone[mt], (uint32_t)(mine - 1) & 1u, abort_flag, err);
+    if (ok && mine > 0) ok = wait_bounded_warp(&ofinal[mt], 0, abort_flag, err);
     ok = __all_sync(0xffffffffu, ok);
     fence_after();
     if (ok) {
@@ -528,52 +558,73 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
 #pragma unroll
       for (int e = 0; e < 2; ++e) id[e] = next[e], next[e] = page_of(i + 2, e);
     }
-  } else if (lane == 0) {
+  } else {
     // ------------------------------------------------ products
-    auto scores = [&](int mt, int st) {
+    // The whole warp goes through the loop, so that addresses and descriptors stay in uniform registers and an issue
+    // is few instructions between the softmax warps' (one lane's branch cost 40% more time per product).
+    const uint64_t q0 = sdesc_k_sw128(q_at), k0 = sdesc_k_sw128(k_at), v0 = sdesc_mn_sw128(v_at, S::kBlock);
+    const uint32_t q_lo = (uint32_t)q0, k_lo = (uint32_t)k0, v_lo = (uint32_t)v0;
+    const uint32_t k_hi = (uint32_t)(k0 >> 32), v_hi = (uint32_t)(v0 >> 32);  // Q's is K's
+    auto scores = [&](auto mt, uint32_t k) {
+      if (elect_one()) {
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const uint32_t in = (k / 4) * S::kBlock;
-        mma_ss(tmem + kS + mt * 128, sdesc_k_sw128(q_at + mt * S::kTile + in) + (uint64_t)(2 * (k % 4)),
-               sdesc_k_sw128(k_at + st * S::kTile + in) + (uint64_t)(2 * (k % 4)), kIdescS, k > 0 ? 1u : 0u);
+        for (int x = 0; x < D / 16; ++x) {
+          const uint32_t in = (x / 4) * (S::kBlock / 16) + 2 * (x % 4);
+          mma_ss(tmem + kS + mt * 128, q_lo + mt * (S::kTile / 16) + in, k_hi, k + in, k_hi, kIdescS, x > 0 ? 1u : 0u);
+        }
+        umma_commit(&sfull[mt]);
       }
-      umma_commit(&sfull[mt]);
+      __syncwarp();
     };
-    bool ok = n == 0 || (wait_bounded(qready, 0, abort_flag, err) && wait_bounded(&kfull[0], 0, abort_flag, err));
+    auto commit = [&](uint64_t* bar) {
+      if (elect_one()) umma_commit(bar);
+      __syncwarp();
+    };
+    bool ok = n == 0 || (wait_bounded_warp(qready, 0, abort_flag, err) && wait_bounded_warp(&kfull[0], 0, abort_flag, err));
     if (ok && n > 0) {
       fence_after();
-      if (n0 > 0) scores(0, 0);
-      if (n1 > 0) scores(1, 0);
-      umma_commit(&kempty[0]);
+      if (n0 > 0) scores(std::integral_constant<int, 0>(), k_lo);
+      if (n1 > 0) scores(std::integral_constant<int, 1>(), k_lo);
+      commit(&kempty[0]);
     }
     for (int i = 0; i < n && ok; ++i) {
       const int st = i & 1, nst = st ^ 1;
-      if (!wait_bounded(&vfull[st], (uint32_t)(i >> 1) & 1u, abort_flag, err)) break;
-      if (i + 1 < n && !wait_bounded(&kfull[nst], (uint32_t)((i + 1) >> 1) & 1u, abort_flag, err)) break;
-      for (int mt = 0; mt < 2; ++mt) {
+      const uint32_t v = v_lo + st * (S::kTile / 16), k = k_lo + nst * (S::kTile / 16);
+      ok = wait_bounded_warp(&vfull[st], (uint32_t)(i >> 1) & 1u, abort_flag, err) &&
+           (i + 1 >= n || wait_bounded_warp(&kfull[nst], (uint32_t)((i + 1) >> 1) & 1u, abort_flag, err));
+      if (!ok) break;
+      auto row_tile = [&](auto mt) {
         const int mine = mt ? n1 : n0;
         if (i < mine) {
-          if (!wait_bounded(&pready[mt], (uint32_t)i & 1u, abort_flag, err)) {
-            ok = false;
-            break;
-          }
-          fence_after();
-          const uint64_t v0 = sdesc_mn_sw128(v_at + st * S::kTile, S::kBlock);
 #pragma unroll
-          for (int k = 0; k < kKeys / 16; ++k)
-            mma_ts(tmem + kO + mt * D, tmem + kS + mt * 128 + 8u * k, v0 + (uint64_t)(128 * k), kIdescO<D>,
-                   (i | k) != 0 ? 1u : 0u);
-          umma_commit(&odone[mt]);
+          for (int half = 0; half < 2; ++half) {
+            if (!wait_bounded_warp(&pready[2 * mt + half], (uint32_t)i & 1u, abort_flag, err)) return false;
+            fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int y = 0; y < kKeys / 32; ++y)
+                mma_ts(tmem + kO + mt * D, tmem + kS + mt * 128 + 32u * half + 8u * y, v + 512u * half + 128u * y, v_hi,
+                       kIdescO<D>, half + y > 0 ? 1u : (uint32_t)(i > 0));
+              umma_commit(&odone[mt]);
+              if (half == 1 && i + 1 == mine) umma_commit(&ofinal[mt]);
+            }
+            __syncwarp();
+          }
+          if (i + 1 < mine) scores(mt, k);
         }
-        if (i + 1 < mine) scores(mt, nst);
-      }
+        return true;
+      };
+      ok = row_tile(std::integral_constant<int, 0>()) && row_tile(std::integral_constant<int, 1>());
       if (!ok) break;
-      umma_commit(&vempty[st]);
-      if (i + 1 < n) umma_commit(&kempty[nst]);
+      commit(&vempty[st]);
+      if (i + 1 < n) commit(&kempty[nst]);
     }
     // all products issued are complete before tensor memory is freed
-    umma_commit(drain);
-    drain_wait(drain, 0, err);
+    if (elect_one()) {
+      umma_commit(drain);
+      drain_wait(drain, 0, err);
+    }
+    __syncwarp();
   }
 
   fence_before();
