@@ -103,6 +103,16 @@ __device__ __forceinline__ void tmem_ld16(uint32_t at, uint32_t (&r)[16]) {
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(at));
 }
+__device__ __forceinline__ void landed(uint32_t (&r)[32], uint32_t (&q)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; i += 8) {
+    asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                      "+r"(r[i + 6]), "+r"(r[i + 7]));
+    asm volatile("" : "+r"(q[i]), "+r"(q[i + 1]), "+r"(q[i + 2]), "+r"(q[i + 3]), "+r"(q[i + 4]), "+r"(q[i + 5]),
+                      "+r"(q[i + 6]), "+r"(q[i + 7]));
+  }
+}
 __device__ __forceinline__ void landed(uint32_t (&r)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
@@ -125,6 +135,11 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   uint32_t d;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 // (a0, a1) * m + c
@@ -340,44 +355,55 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
         // one reading of the half's scores: weights under the reference (-inf: 0 in its place), their sums, the maximum
         auto pass = [&](auto with_mask) {
           const float off = kTop - (ref == -INFINITY ? 0.0f : ref);
-          top = -INFINITY;
-          sum = all = 0.0f;
-          uint32_t s[2][16];
-          tmem_ld16(s_tm + 64 * half, s[0]);
+          // all of the half at once: what lies between two waits for tensor memory is scheduled as one piece
+          uint32_t s[2][32];
+          tmem_ld32_nowait(s_tm + 64 * half, s[0]);
+          tmem_ld32_nowait(s_tm + 64 * half + 32, s[1]);
+          landed(s[0], s[1]);
+          float s0[4], s1[4], m[4];
+          Page page[4];
 #pragma unroll
           for (int grp = 0; grp < 4; ++grp) {
-            landed(s[grp & 1]);
-            if (grp < 3) tmem_ld16(s_tm + 64 * half + 16 * (grp + 1), s[(grp + 1) & 1]);
+            page[grp] = page_at(pages, 4 * half + grp, q_scale, q_sum);
             float v[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(s[grp & 1][e]);
-            const Page p = page_at(pages, 4 * half + grp, q_scale, q_sum);
+            for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(s[grp >> 1][16 * (grp & 1) + e]);
             if constexpr (!decltype(with_mask)::value) {
-              float m0 = v[0], m1 = v[1];
+              float m0 = max3(v[0], v[1], v[2]), m1 = max3(v[3], v[4], v[5]);
 #pragma unroll
-              for (int e = 2; e < 16; e += 2) m0 = fmaxf(m0, v[e]), m1 = fmaxf(m1, v[e + 1]);
-              top = fmaxf(top, fmaf(fmaxf(m0, m1), p.f2, p.c));
+              for (int e = 6; e < 14; e += 4) m0 = max3(m0, v[e], v[e + 1]), m1 = max3(m1, v[e + 2], v[e + 3]);
+              m[grp] = fmaf(fmaxf(max3(m0, v[14], v[15]), m1), page[grp].f2, page[grp].c);
             }
 #pragma unroll
-            for (int e = 0; e < 16; e += 2) fma2(v[e], v[e + 1], p.f2, p.c + off);
+            for (int e = 0; e < 16; e += 2) fma2(v[e], v[e + 1], page[grp].f2, page[grp].c + off);
             if constexpr (decltype(with_mask)::value) {
+              m[grp] = -INFINITY;
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
                 if (64 * half + 16 * grp + e >= lim) v[e] = -INFINITY;
-                top = fmaxf(top, v[e] - off);
+                m[grp] = fmaxf(m[grp], v[e] - off);
               }
             }
 #pragma unroll
             for (int e = 0; e < 16; ++e) v[e] = ex2(v[e]);
-            float s0 = v[0], s1 = v[1];
+            s0[grp] = v[0], s1[grp] = v[1];
 #pragma unroll
-            for (int e = 2; e < 16; e += 2) add2(s0, s1, v[e], v[e + 1]);
-            s0 += s1;
-            sum = fmaf(s0, p.inv, sum);
+            for (int e = 2; e < 16; e += 2) add2(s0[grp], s1[grp], v[e], v[e + 1]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[grp][e] = pack2(v[2 * e], v[2 * e + 1]);
+          }
+          top = fmaxf(max3(m[0], m[1], m[2]), m[3]);
+          sum = all = 0.0f;
+#pragma unroll
+          for (int grp = 0; grp < 4; ++grp) {
+            const float both = s0[grp] + s1[grp];
+            sum = fmaf(both, page[grp].inv, sum);
             // a page whose values are all zero takes part in the sum alone
-            all += p.some ? s0 : 0.0f;
+            all += page[grp].some ? both : 0.0f;
+            if (!page[grp].some) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) w[grp][e] = p.some ? pack2(v[2 * e], v[2 * e + 1]) : 0u;
+              for (int e = 0; e < 8; ++e) w[grp][e] = 0u;
+            }
           }
         };
         auto run = [&] {
