@@ -50,7 +50,7 @@ constexpr int kMeta = 4;                  // slots of page scales
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kS = 0, kO = 256;      // tensor memory columns: S0 and S1 (W in their place), O0 and O1
 constexpr float kTop = 7.0f;              // log2 of the weight at the reference maximum
-constexpr float kSlack = 8.0f;            // what the maximum may grow by before the reference follows
+constexpr float kMost = 32768.0f;         // what the weights of half a tile may add up to before the reference follows
 constexpr float kLog2e = 1.4426950408889634f;
 
 // kind::f16, D f32, A and B fp16, M = 128: scores (both K-major, N = 128 tokens), outputs (B MN-major, N = D)
@@ -135,11 +135,6 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   uint32_t d;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 // (a0, a1) * m + c
@@ -350,72 +345,78 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
       // the tile in two halves, so that the products of the first begin while the second is worked on
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {
+        const uint32_t from = s_tm + 64 * half;
+        const int first = 64 * half;
         uint32_t w[4][8];
-        float top, sum, all;
-        // one reading of the half's scores: weights under the reference (-inf: 0 in its place), their sums, the maximum
-        auto pass = [&](auto with_mask) {
+        float sum, all, most;
+        // one reading of the half's scores: weights under the reference (-inf: 0 in its place) and their sums
+        auto weigh = [&](auto with_mask) {
           const float off = kTop - (ref == -INFINITY ? 0.0f : ref);
           // all of the half at once: what lies between two waits for tensor memory is scheduled as one piece
           uint32_t s[2][32];
-          tmem_ld32_nowait(s_tm + 64 * half, s[0]);
-          tmem_ld32_nowait(s_tm + 64 * half + 32, s[1]);
+          tmem_ld32_nowait(from, s[0]);
+          tmem_ld32_nowait(from + 32, s[1]);
           landed(s[0], s[1]);
-          float s0[4], s1[4], m[4];
-          Page page[4];
+          sum = all = most = 0.0f;
 #pragma unroll
           for (int grp = 0; grp < 4; ++grp) {
-            page[grp] = page_at(pages, 4 * half + grp, q_scale, q_sum);
+            const Page p = page_at(pages, 4 * half + grp, q_scale, q_sum);
             float v[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(s[grp >> 1][16 * (grp & 1) + e]);
-            if constexpr (!decltype(with_mask)::value) {
-              float m0 = max3(v[0], v[1], v[2]), m1 = max3(v[3], v[4], v[5]);
 #pragma unroll
-              for (int e = 6; e < 14; e += 4) m0 = max3(m0, v[e], v[e + 1]), m1 = max3(m1, v[e + 2], v[e + 3]);
-              m[grp] = fmaf(fmaxf(max3(m0, v[14], v[15]), m1), page[grp].f2, page[grp].c);
-            }
-#pragma unroll
-            for (int e = 0; e < 16; e += 2) fma2(v[e], v[e + 1], page[grp].f2, page[grp].c + off);
+            for (int e = 0; e < 16; e += 2) fma2(v[e], v[e + 1], p.f2, p.c + off);
             if constexpr (decltype(with_mask)::value) {
-              m[grp] = -INFINITY;
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                if (64 * half + 16 * grp + e >= lim) v[e] = -INFINITY;
-                m[grp] = fmaxf(m[grp], v[e] - off);
-              }
+              for (int e = 0; e < 16; ++e)
+                if (first + 16 * grp + e >= lim) v[e] = -INFINITY;
             }
 #pragma unroll
             for (int e = 0; e < 16; ++e) v[e] = ex2(v[e]);
-            s0[grp] = v[0], s1[grp] = v[1];
+            float s0 = v[0], s1 = v[1];
 #pragma unroll
-            for (int e = 2; e < 16; e += 2) add2(s0[grp], s1[grp], v[e], v[e + 1]);
+            for (int e = 2; e < 16; e += 2) add2(s0, s1, v[e], v[e + 1]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) w[grp][e] = pack2(v[2 * e], v[2 * e + 1]);
-          }
-          top = fmaxf(max3(m[0], m[1], m[2]), m[3]);
-          sum = all = 0.0f;
-#pragma unroll
-          for (int grp = 0; grp < 4; ++grp) {
-            const float both = s0[grp] + s1[grp];
-            sum = fmaf(both, page[grp].inv, sum);
+            s0 += s1;
+            most += s0;
+            sum = fmaf(s0, p.inv, sum);
             // a page whose values are all zero takes part in the sum alone
-            all += page[grp].some ? both : 0.0f;
-            if (!page[grp].some) {
+            all += p.some ? s0 : 0.0f;
+            if (!p.some) {
 #pragma unroll
               for (int e = 0; e < 8; ++e) w[grp][e] = 0u;
             }
           }
         };
+        // the row's maximum over the half (in log2 units, values' scale included)
+        auto maximum = [&] {
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int grp = 0; grp < 4; ++grp) {
+            const Page p = page_at(pages, 4 * half + grp, q_scale, q_sum);
+            uint32_t s[16];
+            tmem_ld16(from + 16 * grp, s);
+            landed(s);
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (first + 16 * grp + e < lim) top = fmaxf(top, fmaf(__uint_as_float(s[e]), p.f2, p.c));
+          }
+          return top;
+        };
         auto run = [&] {
           if (masked)
-            pass(std::true_type());
+            weigh(std::true_type());
           else
-            pass(std::false_type());
+            weigh(std::false_type());
         };
         run();
-        const bool follow = top > ref + kSlack || (ref == -INFINITY && top > -INFINITY);
+        // No weight is above the sum of the half's: while that is at most 2^15 the reference holds, and no maximum is
+        // taken.  Above it (an infinity with it), and until a row has seen a token, the reference moves.
+        const bool follow = most > kMost || ref == -INFINITY;
         if (__any_sync(0xffffffffu, follow)) {
-          const float next = follow ? top : ref;
+          const float top = maximum();
+          const float next = follow ? fmaxf(ref, top) : ref;
           const float grow = ref == -INFINITY ? 0.0f : ex2(ref - next);
           if (i + half > 0) {
             // the products up to the half before this one (the one before that is known to have ended)
@@ -425,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
             }
             __syncwarp();
             fence_after();
-            const float by = follow ? grow : 1.0f;
+            const float by = follow && next != ref ? grow : 1.0f;
 #pragma unroll 1
             for (int x = 0; x < D; x += 16) {
               uint32_t r[16];
@@ -436,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
               tmem_st16(o_tm + x, r);
             }
           }
-          if (follow) {
+          if (follow && next != ref) {
             l *= grow;
             ws *= grow;
             ref = next;
@@ -527,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
           asm("add.rn.f16x2 %0, %1, %2;" : "=r"(o[2 * e]) : "r"(__byte_perm(w[e], 0x64646464u, 0x4140u)), "r"(minus));
           asm("add.rn.f16x2 %0, %1, %2;" : "=r"(o[2 * e + 1]) : "r"(__byte_perm(w[e], 0x64646464u, 0x4342u)), "r"(minus));
         }
-        if (!there) {
+        if (!there) {  // the warp's tokens of one page: a branch for all lanes
 #pragma unroll
           for (int e = 0; e < 8; ++e) o[e] = 0u;
         }
