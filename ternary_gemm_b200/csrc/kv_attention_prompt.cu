@@ -183,6 +183,19 @@ struct Item {
   int keys, pos0;        // tokens that the table can hold; position of the request's first row
 };
 
+// Rows r, r + step, ... in (row of the batch, head of the group) order, with
+// the divisions by the group's size taken once.
+struct Walk {
+  int tok, head, g, tok_step, head_step;
+  __device__ __forceinline__ Walk(int r, int step, int group)
+      : tok(r / group), head(r % group), g(group), tok_step(step / group), head_step(step % group) {}
+  __device__ __forceinline__ void next() {
+    tok += tok_step;
+    head += head_step;
+    if (head >= g) head -= g, ++tok;
+  }
+};
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const KvAttentionArgs a, int* err) {
   using S = Shape<D>;
@@ -288,16 +301,32 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_tm = tmem + kS + mt * 128 + lanes, o_tm = tmem + kO + mt * D + lanes;
     const float scale = a.scale ? *a.scale : rsqrtf((float)D);
+    // The warp's rows: copied by neighbouring lanes into their places, then turned to fp16 there, a row's largest value
+    // in [2^10, 2^11), by the row's thread.  In short loops: the code runs once a CTA, and fetching it costs most.
     float q_scale, q_sum = 0.0f;
     {
-      // the row into fp16, its largest value in [2^10, 2^11)
-      const uint16_t* q = reinterpret_cast<const uint16_t*>(a.q) +
-                          (live ? (int64_t)(it.row0 + row / g) * a.q_stride + ((int64_t)h * g + row % g) * D : 0);
-      const uint4* from = reinterpret_cast<const uint4*>(q);
+      constexpr int kLanes = D / 8, kStep = 32 / kLanes;  // lanes per row, rows per copy
+      const uint32_t tile = q_at + mt * S::kTile;
+      const int piece = lane % kLanes, t0 = (warp & 3) * 32 + lane / kLanes, r0 = it.first + mt * kRowsM + t0;
+      const uint16_t* q = reinterpret_cast<const uint16_t*>(a.q) + (int64_t)it.row0 * a.q_stride + (int64_t)h * g * D + piece * 8;
+      Walk at(r0, kStep, g);
+#pragma unroll 2
+      for (int x = 0; x < kLanes; ++x) {
+        const bool there = r0 + x * kStep < rows;
+        const uint16_t* from = there ? q + (int64_t)at.tok * a.q_stride + at.head * D : q;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                         tile + (piece / 8) * S::kBlock + swizzled(t0 + x * kStep, piece % 8)),
+                     "l"(from), "r"(there ? 16 : 0)
+                     : "memory");
+        at.next();
+      }
+      asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+      __syncwarp();
+      const int t = (warp & 3) * 32 + lane;
       uint32_t top = 0;
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        const uint4 v = live ? __ldg(from + i) : make_uint4(0, 0, 0, 0);
+#pragma unroll 4
+      for (int i = 0; i < kLanes; ++i) {
+        const uint4 v = lds128(tile + (i / 8) * S::kBlock + swizzled(t, i % 8));
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -308,10 +337,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
       const float up = __uint_as_float((uint32_t)(127 + 10 - e2) << 23), down = __uint_as_float((uint32_t)(127 - 10 + e2) << 23);
       const float sign = scale < 0.0f ? -up : up;
       q_scale = fabsf(scale) * kLog2e * down;
-      const int t = (warp & 3) * 32 + lane;
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        const uint4 v = live ? __ldg(from + i) : make_uint4(0, 0, 0, 0);
+#pragma unroll 2
+      for (int i = 0; i < kLanes; ++i) {
+        const uint32_t place = tile + (i / 8) * S::kBlock + swizzled(t, i % 8);
+        const uint4 v = lds128(place);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
         uint32_t o[4];
 #pragma unroll
@@ -320,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
           const __half2 hv = *reinterpret_cast<const __half2*>(&o[e]);
           q_sum += __low2float(hv) + __high2float(hv);
         }
-        sts128(q_at + mt * S::kTile + (i / 8) * S::kBlock + swizzled(t, i % 8), o[0], o[1], o[2], o[3]);
+        sts128(place, o[0], o[1], o[2], o[3]);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -466,7 +495,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
     fence_after();
     if (ok) {
       const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
-      const int64_t at = live ? ((int64_t)(it.row0 + row / g) * a.Hq + (int64_t)h * g + row % g) * D : 0;
+      // through the warp's part of the Q tile, whose products have ended, so that lanes write whole rows
+      const uint32_t stage = q_at + mt * S::kTile + (warp & 3) * (32 * D * 2);
+      constexpr int kLanes = D / 8;
+      auto place = [&](int r, int piece) { return stage + r * (D * 2) + ((piece ^ (r & 7)) << 4); };
 #pragma unroll 1
       for (int x = 0; x < D; x += 16) {
         uint32_t r[16];
@@ -477,19 +509,32 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
         }
 #pragma unroll
         for (int e = 0; e < 16; ++e) v[e] = mine > 0 ? fmaf(2.0f, __uint_as_float(r[e]), ws) * inv : 0.0f;
-        if (live && a.o_bf16) {
+        if (a.o_bf16) {
           uint32_t p[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(p[e]) : "f"(v[2 * e + 1]), "f"(v[2 * e]));
-          uint4* to = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.o) + at + x);
-          to[0] = make_uint4(p[0], p[1], p[2], p[3]);
-          to[1] = make_uint4(p[4], p[5], p[6], p[7]);
+          sts128(place(lane, x / 8), p[0], p[1], p[2], p[3]);
+          sts128(place(lane, x / 8 + 1), p[4], p[5], p[6], p[7]);
         } else if (live) {
+          const int64_t at = ((int64_t)(it.row0 + row / g) * a.Hq + (int64_t)h * g + row % g) * D;
           float4* to = reinterpret_cast<float4*>(reinterpret_cast<float*>(a.o) + at + x);
 #pragma unroll
           for (int e = 0; e < 4; ++e) to[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
         }
         __syncwarp();
+      }
+      if (a.o_bf16) {
+        constexpr int kStep = 32 / kLanes;
+        const int r0 = it.first + mt * kRowsM + (warp & 3) * 32 + lane / kLanes;
+        Walk to(r0, kStep, g);
+#pragma unroll 2
+        for (int x = 0; x < kLanes; ++x) {
+          const uint4 v = lds128(place(x * kStep + lane / kLanes, lane % kLanes));
+          if (r0 + x * kStep < rows)
+            *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.o) +
+                                      ((int64_t)(it.row0 + to.tok) * a.Hq + (int64_t)h * g + to.head) * D + lane % kLanes * 8) = v;
+          to.next();
+        }
       }
     }
   } else if (warp < 12) {
