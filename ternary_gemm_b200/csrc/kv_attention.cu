@@ -876,7 +876,7 @@ cudaError_t launch_d(const KvAttentionArgs& a, cudaStream_t stream) {
 
 size_t kv_attention_workspace(int64_t T, int Hq, int Hkv, int D, int B) {
   (void)T, (void)Hq, (void)Hkv, (void)B;
-  size_t most = 0;
+  size_t most = D == 64 || D == 128 ? kv_attention_prompt_workspace(D) : 0;
   for (int NT = 1; NT <= 2; ++NT) {
     const size_t workers = (size_t)sm100_host::sm_count() * blocks_per_sm(D, NT, false) * kWarps;
     const size_t bytes = workers * (2 * 8 * NT * (D * 4 + 8) + sizeof(Record));

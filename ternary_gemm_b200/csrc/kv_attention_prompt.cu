@@ -28,6 +28,7 @@
 //                   under the other's products
 // Every mbarrier wait is bounded; a CTA that gives up sets the device error
 // word, waits for its products and frees its tensor memory.
+#include <algorithm>
 #include <cstdint>
 
 #include <cuda_bf16.h>
@@ -47,6 +48,8 @@ constexpr int kRows = 2 * kRowsM;         // rows of a CTA
 constexpr int kKeys = 128;                // tokens of a tile
 constexpr int kThreads = 13 * 32;
 constexpr int kMeta = 4;                  // slots of page scales
+constexpr int kMostSplits = 32;           // CTAs that share an item's tokens at most
+constexpr int kLeastTiles = 4;            // and the tiles that each of them has at least
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kS = 0, kO = 256;      // tensor memory columns: S0 and S1 (W in their place), O0 and O1
 constexpr float kTop = 7.0f;              // log2 of the weight at the reference maximum
@@ -92,6 +95,13 @@ __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
   return p != 0;
+}
+
+// A bounded wait of the whole warp, with one answer for all its lanes (the
+// limit may run out for some while others see the phase end).
+__device__ __forceinline__ bool await(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err) {
+  const bool there = wait_bounded_warp(bar, parity, abort_flag, err);
+  return __all_sync(0xffffffffu, there) != 0;
 }
 
 // sixteen columns of this thread's lane; the registers hold them after landed()
@@ -196,8 +206,28 @@ struct Walk {
   }
 };
 
+// What the CTAs leave in the workspace where several share an item: for each
+// row (reference, sum of the weights over it) and its outputs unscaled, and for
+// each item what the joining kernel has to know (parts 0: nothing to join).
+struct Joined {
+  int first, rows, row0, h, parts;
+};
+struct Parts {
+  float* o;         // [CTAs][256][D]
+  float2* ml;       // [CTAs][256]
+  Joined* item;     // [items]
+};
+__host__ __device__ inline Parts parts_of(void* workspace, int64_t ctas, int D) {
+  Parts p;
+  p.o = reinterpret_cast<float*>(workspace);
+  p.ml = reinterpret_cast<float2*>(p.o + (size_t)ctas * kRows * D);
+  p.item = reinterpret_cast<Joined*>(p.ml + (size_t)ctas * kRows);
+  return p;
+}
+
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const KvAttentionArgs a, int* err) {
+__global__ void __launch_bounds__(kThreads, 1)
+kv_attention_prompt_kernel(const KvAttentionArgs a, const int splits, int* err) {
   using S = Shape<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -215,8 +245,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
 
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int g = a.Hq / a.Hkv;
-  const int h = blockIdx.x % a.Hkv;
-  const int64_t rank = blockIdx.x / a.Hkv;
+  const int split = blockIdx.x % splits, h = blockIdx.x / splits % a.Hkv;
+  const int64_t rank = blockIdx.x / splits / a.Hkv;
+  const Parts parts = parts_of(a.workspace, gridDim.x, D);
 
   // ---- which 256 rows: the request whose row tiles hold this CTA's rank
   {
@@ -256,7 +287,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
     __syncthreads();
   }
   const Item it = item;
-  if (it.b < 0) return;
+  // tokens that the last row of a tile sees, in tiles
+  const int rows = it.n * g;
+  auto tiles_of = [&](int mt) {
+    const int last = min(it.first + (mt + 1) * kRowsM, rows) - 1;
+    if (last < it.first + mt * kRowsM) return 0;
+    const int sees = min(it.pos0 + last / g + 1, it.keys);
+    return sees > 0 ? (sees - 1) / kKeys + 1 : 0;
+  };
+  const int seen0 = it.b < 0 ? 0 : tiles_of(0), seen1 = it.b < 0 ? 0 : tiles_of(1), seen = max(seen0, seen1);
+  // this CTA's share of them
+  const int used = min(splits, max(seen / kLeastTiles, 1));
+  if (splits > 1 && split == 0 && tid == 0)
+    parts.item[blockIdx.x / splits] = {it.first, min(rows - it.first, kRows), it.row0, h, it.b < 0 || used == 1 ? 0 : used};
+  if (it.b < 0 || split >= used) return;
+  const int i0 = (int)((int64_t)seen * split / used), i1 = (int)((int64_t)seen * (split + 1) / used);
+  const int n0 = max(min(seen0, i1) - i0, 0), n1 = max(min(seen1, i1) - i0, 0), n = max(n0, n1);
+  const int tok0 = i0 * kKeys;
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -282,16 +329,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
   __syncthreads();
   fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-
-  // tokens that the last row of a tile sees, in tiles
-  const int rows = it.n * g;
-  auto tiles_of = [&](int mt) {
-    const int last = min(it.first + (mt + 1) * kRowsM, rows) - 1;
-    if (last < it.first + mt * kRowsM) return 0;
-    const int sees = min(it.pos0 + last / g + 1, it.keys);
-    return sees > 0 ? (sees - 1) / kKeys + 1 : 0;
-  };
-  const int n0 = tiles_of(0), n1 = tiles_of(1), n = max(n0, n1);
 
   if (warp < 8) {
     // ------------------------------------------------ softmax: one row per thread
@@ -358,15 +395,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
 
     float ref = -INFINITY, l = 0.0f, ws = 0.0f;
     // tokens that the row sees; rows that are none see all (their scores are 0)
-    const int sees = live ? min(it.pos0 + row / g + 1, it.keys) : INT32_MAX;
+    const int sees = live ? min(it.pos0 + row / g + 1, it.keys) - tok0 : INT32_MAX;
     bool ok = true;
     for (int i = 0; i < mine; ++i) {
-      if (!wait_bounded_warp(&mready[i % kMeta], (uint32_t)(i / kMeta) & 1u, abort_flag, err) ||
-          !wait_bounded_warp(&sfull[mt], (uint32_t)i & 1u, abort_flag, err)) {
+      if (!await(&mready[i % kMeta], (uint32_t)(i / kMeta) & 1u, abort_flag, err) ||
+          !await(&sfull[mt], (uint32_t)i & 1u, abort_flag, err)) {
         ok = false;
         break;
       }
-      __syncwarp();
       fence_after();
       const int lim = sees - i * kKeys;
       const bool masked = __any_sync(0xffffffffu, lim < kKeys);
@@ -449,11 +485,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
           const float grow = ref == -INFINITY ? 0.0f : ex2(ref - next);
           if (i + half > 0) {
             // the products up to the half before this one (the one before that is known to have ended)
-            if (!wait_bounded_warp(&odone[mt], (uint32_t)(half ^ 1), abort_flag, err)) {
+            if (!await(&odone[mt], (uint32_t)(half ^ 1), abort_flag, err)) {
               ok = false;
               break;
             }
-            __syncwarp();
             fence_after();
             const float by = follow && next != ref ? grow : 1.0f;
 #pragma unroll 1
@@ -490,10 +525,30 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
       if (!ok) break;
     }
     // ---- o = (2 O + sum of the weights) / l
-    if (ok && mine > 0) ok = wait_bounded_warp(&ofinal[mt], 0, abort_flag, err);
-    ok = __all_sync(0xffffffffu, ok);
+    if (ok && mine > 0) ok = await(&ofinal[mt], 0, abort_flag, err);
     fence_after();
-    if (ok) {
+    if (ok && used > 1) {
+      // a part: unscaled, under this CTA's reference
+      const int t = mt * kRowsM + (warp & 3) * 32 + lane;
+      float4* to = reinterpret_cast<float4*>(parts.o + ((int64_t)blockIdx.x * kRows + t) * D);
+#pragma unroll 1
+      for (int x = 0; x < D; x += 16) {
+        uint32_t r[16];
+        if (mine > 0) {
+          tmem_ld16(o_tm + x, r);
+          landed(r);
+        }
+        float v[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = mine > 0 ? fmaf(2.0f, __uint_as_float(r[e]), ws) : 0.0f;
+        if (live) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) to[x / 4 + e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+        }
+        __syncwarp();
+      }
+      if (live) parts.ml[(int64_t)blockIdx.x * kRows + t] = make_float2(ref, l);
+    } else if (ok) {
       const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
       // through the warp's part of the Q tile, whose products have ended, so that lanes write whole rows
       const uint32_t stage = q_at + mt * S::kTile + (warp & 3) * (32 * D * 2);
@@ -546,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
     const int L = (1 << a.bits) - 1;
     const uint32_t minus = 0xE400E400u | ((uint32_t)(1 << (a.bits - 1)) * 0x10001u);  // -(1024 + z), twice
     auto page_of = [&](int i, int grp) {
-      const int tok = i * kKeys + cw * 32 + grp * 16;
+      const int tok = tok0 + i * kKeys + cw * 32 + grp * 16;
       const int v = i < n && tok < it.keys ? pages[tok >> block_shift] : -1;
       return v >= 0 && v < a.num_blocks ? v : -1;
     };
@@ -557,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
         const int half = j % kPerHalf, tok = (j / kPerHalf) * 8 + my_tok;   // tok < 32
         const int page = id[(j / kPerHalf) >> 1];
         const int64_t from =
-            (((int64_t)page * a.Hkv + h) * a.block + ((i * kKeys + cw * 32 + tok) & (a.block - 1))) * D + half * 64 + my_piece * 16;
+            (((int64_t)page * a.Hkv + h) * a.block + ((tok0 + i * kKeys + cw * 32 + tok) & (a.block - 1))) * D + half * 64 + my_piece * 16;
         v[j] = page >= 0 ? *reinterpret_cast<const uint4*>(codes + from) : make_uint4(0, 0, 0, 0);
       }
     };
@@ -600,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
     for (int i = 0; i < n; ++i) {
       const int st = i & 1;
       const uint32_t reuse = ((uint32_t)(i >> 1) & 1u) ^ 1u;
-      if (!wait_bounded_warp(&kempty[st], reuse, abort_flag, err)) break;
+      if (!await(&kempty[st], reuse, abort_flag, err)) break;
       if (lane < 2) {
         const bool there = (lane == 0 ? id[0] : id[1]) >= 0;
         const float vu = __fdiv_rn(vs, (float)L);
@@ -621,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
         load(a.k_codes, i + 1, next, kv);
         scales(next);
       }
-      if (!wait_bounded_warp(&vempty[st], reuse, abort_flag, err)) break;
+      if (!await(&vempty[st], reuse, abort_flag, err)) break;
       convert(v_at + st * S::kTile, id, vv);
       fence_proxy_async_smem();
       __syncwarp();
@@ -652,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
       if (elect_one()) umma_commit(bar);
       __syncwarp();
     };
-    bool ok = n == 0 || (wait_bounded_warp(qready, 0, abort_flag, err) && wait_bounded_warp(&kfull[0], 0, abort_flag, err));
+    bool ok = n == 0 || (await(qready, 0, abort_flag, err) && await(&kfull[0], 0, abort_flag, err));
     if (ok && n > 0) {
       fence_after();
       if (n0 > 0) scores(std::integral_constant<int, 0>(), k_lo);
@@ -662,15 +717,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
     for (int i = 0; i < n && ok; ++i) {
       const int st = i & 1, nst = st ^ 1;
       const uint32_t v = v_lo + st * (S::kTile / 16), k = k_lo + nst * (S::kTile / 16);
-      ok = wait_bounded_warp(&vfull[st], (uint32_t)(i >> 1) & 1u, abort_flag, err) &&
-           (i + 1 >= n || wait_bounded_warp(&kfull[nst], (uint32_t)((i + 1) >> 1) & 1u, abort_flag, err));
+      ok = await(&vfull[st], (uint32_t)(i >> 1) & 1u, abort_flag, err) &&
+           (i + 1 >= n || await(&kfull[nst], (uint32_t)((i + 1) >> 1) & 1u, abort_flag, err));
       if (!ok) break;
       auto row_tile = [&](auto mt) {
         const int mine = mt ? n1 : n0;
         if (i < mine) {
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            if (!wait_bounded_warp(&pready[2 * mt + half], (uint32_t)i & 1u, abort_flag, err)) return false;
+            if (!await(&pready[2 * mt + half], (uint32_t)i & 1u, abort_flag, err)) return false;
             fence_after();
             if (elect_one()) {
 #pragma unroll
@@ -705,6 +760,74 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
   if (warp == 12) tmem_dealloc(tmem, kTmemCols);
 }
 
+// Joins the parts of a row, in order: a CTA takes 32 rows of an item, a warp
+// one row after the other.
+template <int D>
+__global__ void __launch_bounds__(256) kv_attention_prompt_join_kernel(const KvAttentionArgs a, const int splits) {
+  constexpr int V = D / 32;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t items = gridDim.x / (kRows / 32), at = blockIdx.x / (kRows / 32);
+  const Parts parts = parts_of(a.workspace, items * splits, D);
+  const Joined it = parts.item[at];
+  if (it.parts == 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = a.Hq / a.Hkv;
+  const int first = (blockIdx.x % (kRows / 32)) * 32;
+  for (int t = first + warp; t < min(first + 32, it.rows); t += 8) {
+    auto slot = [&](int p) { return (at * splits + p) * kRows + t; };
+    const float2 ml = lane < it.parts ? parts.ml[slot(lane)] : make_float2(-INFINITY, 0.0f);
+    float top = ml.x;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float f = ex2(ml.x - (top == -INFINITY ? 0.0f : top));
+    float sum = f * ml.y;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    float acc[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+#pragma unroll 4
+    for (int p = 0; p < it.parts; ++p) {
+      const float by = __shfl_sync(0xffffffffu, f, p);
+      const float* from = parts.o + slot(p) * D + lane * V;
+#pragma unroll
+      for (int i = 0; i < V; i += 2) {
+        const float2 v = *reinterpret_cast<const float2*>(from + i);
+        acc[i] = fmaf(by, v.x, acc[i]);
+        acc[i + 1] = fmaf(by, v.y, acc[i + 1]);
+      }
+    }
+    const float inv = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
+    const int row = it.first + t;
+    const int64_t to = ((int64_t)(it.row0 + row / g) * a.Hq + (int64_t)it.h * g + row % g) * D + lane * V;
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+      const float x = acc[i] * inv, y = acc[i + 1] * inv;
+      if (a.o_bf16) {
+        uint32_t p;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(p) : "f"(y), "f"(x));
+        *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(a.o) + to + i) = p;
+      } else {
+        *reinterpret_cast<float2*>(reinterpret_cast<float*>(a.o) + to + i) = make_float2(x, y);
+      }
+    }
+  }
+}
+
+// How a batch is laid out: a CTA for each row tile that it can have, whatever
+// its rows' split over the requests, and as many CTAs per item as fill the SMs
+// where there are few items and the table is long.
+struct Layout {
+  int64_t items;
+  int splits;
+};
+Layout layout_of(const KvAttentionArgs& a) {
+  Layout l;
+  l.items = ((a.T * (a.Hq / a.Hkv) + kRows - 1) / kRows + a.B - 1) * a.Hkv;
+  const int64_t room = sm100_host::sm_count() / l.items, tiles = a.width * a.block / kKeys / kLeastTiles;
+  l.splits = (int)std::max<int64_t>(1, std::min({room, tiles, (int64_t)kMostSplits}));
+  return l;
+}
+
 template <int D>
 cudaError_t launch(const KvAttentionArgs& a, cudaStream_t stream) {
   int* err = device_error_word();
@@ -712,17 +835,39 @@ cudaError_t launch(const KvAttentionArgs& a, cudaStream_t stream) {
   static std::atomic<bool> done[sm100_host::kMaxDevices];
   cudaError_t e = sm100_host::ensure_smem(kv_attention_prompt_kernel<D>, (int)Shape<D>::kSmem, done);
   if (e != cudaSuccess) return e;
-  // a CTA for each row tile that the batch can have, whatever its rows' split over the requests
-  const int64_t tiles = (a.T * (a.Hq / a.Hkv) + kRows - 1) / kRows + a.B;
-  kv_attention_prompt_kernel<D><<<(unsigned)(tiles * a.Hkv), kThreads, Shape<D>::kSmem, stream>>>(a, err);
-  return cudaGetLastError();
+  const Layout l = layout_of(a);
+  kv_attention_prompt_kernel<D><<<(unsigned)(l.items * l.splits), kThreads, Shape<D>::kSmem, stream>>>(a, l.splits, err);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || l.splits == 1) return e;
+  return sm100_host::launch_pdl(kv_attention_prompt_join_kernel<D>, (unsigned)(l.items * (kRows / 32)), 256, 0, stream, 1,
+                                a, l.splits);
 }
 
 }  // namespace
 
+// The tensor cores' tiles pay where enough of them are at work and full.  With
+// P the CTAs at once times the share of their 256 rows that is used (on
+// average over the requests), the measured times cross at P near 18, or 45
+// where CTAs share their items' tokens (a share costs its CTA about 12 us of
+// start and end and the join).  At 32 heads over 8 and 64 requests of 4096
+// tokens: about 25 rows a head and request, P = 15, 181 us here against 152 in
+// kv_attention.cu; 50 rows, P = 28, 192 against 277.  One request of 16384,
+// shared: 64 rows, P = 36, 48 us against 41; 128 rows, P = 72, 48 against 62;
+// 1024 rows, 95 against 347.
+constexpr int64_t kWorkAlone = 18, kWorkShared = 45;
 bool kv_attention_prompt_supports(const KvAttentionArgs& a) {
-  return a.q_bf16 && (a.D == 64 || a.D == 128) && a.T * (a.Hq / a.Hkv) >= kPromptRows * (int64_t)a.B &&
-         (a.T * (a.Hq / a.Hkv) / kRows + 1 + a.B) * a.Hkv <= INT32_MAX;
+  if (!a.q_bf16 || (a.D != 64 && a.D != 128)) return false;
+  const int64_t rows = a.T * (a.Hq / a.Hkv);
+  const Layout l = layout_of(a);
+  if (l.items * l.splits > INT32_MAX / (kRows / 32)) return false;
+  const int64_t tiles = std::max((rows / a.B + kRows - 1) / kRows, (int64_t)1) * a.B;  // of equal requests
+  const int64_t ctas = std::min(tiles * a.Hkv * l.splits, (int64_t)sm100_host::sm_count());
+  return rows * ctas >= (l.splits == 1 ? kWorkAlone : kWorkShared) * tiles * kRows;
+}
+
+size_t kv_attention_prompt_workspace(int D) {
+  const size_t ctas = (size_t)sm100_host::sm_count();  // items are split over CTAs only as far as there are SMs
+  return ctas * (kRows * (D * 4 + 8) + sizeof(Joined));
 }
 
 cudaError_t launch_kv_attention_prompt(const KvAttentionArgs& a, cudaStream_t stream) {

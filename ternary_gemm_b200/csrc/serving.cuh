@@ -63,9 +63,10 @@ struct KvAttentionArgs {
 size_t kv_attention_workspace(int64_t T, int Hq, int Hkv, int D, int B);
 cudaError_t launch_kv_attention(const KvAttentionArgs& a, cudaStream_t stream);
 // The same with 256-row tiles on tcgen05 (kv_attention_prompt.cu), for bf16
-// queries from kPromptRows rows per request and cached head on average.
-constexpr int64_t kPromptRows = 64;
+// queries of head dimension 64 or 128 where enough full row tiles' worth of
+// CTAs are at work at once.
 bool kv_attention_prompt_supports(const KvAttentionArgs& a);
+size_t kv_attention_prompt_workspace(int D);
 cudaError_t launch_kv_attention_prompt(const KvAttentionArgs& a, cudaStream_t stream);
 
 cudaError_t launch_add_rms_quant(const void* x, const void* residual, bool bf16, int64_t M, int64_t K,

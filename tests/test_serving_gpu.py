@@ -265,6 +265,16 @@ def test_attention_prompt_shapes(H, D, block, Hq, Hkv):
     _attend(H, np.random.default_rng(D + Hq), [150, 37, 260], np.array([150, 137, 400]), Hq, Hkv, D, block, 8, True)
 
 
+@pytest.mark.parametrize("o_bf16", [True, False])
+@pytest.mark.parametrize("D,Hq,Hkv,new,total", [(128, 8, 2, [64], [2100]), (128, 8, 2, [130, 2], [1500, 3700]),
+                                                (64, 6, 1, [700], [700]), (64, 4, 4, [300, 0, 90], [4200, 0, 90]),
+                                                (128, 16, 4, [257], [2000])])
+def test_attention_prompts_over_many_ctas(H, D, Hq, Hkv, new, total, o_bf16):
+    """Few row tiles over long contexts, which several CTAs share: rows that see nothing of a CTA's tokens, requests
+    too short to be shared beside long ones."""
+    _attend(H, np.random.default_rng(D + sum(new)), new, np.array(total), Hq, Hkv, D, 64, 8, True, o_bf16, pad=3)
+
+
 def test_attention_rows_without_tokens_and_padding(H):
     """Requests of no rows, lengths of 0, more rows than tokens, rows before and behind the requests."""
     rng = np.random.default_rng(5)
