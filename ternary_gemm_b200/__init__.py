@@ -462,7 +462,7 @@ def hbl_gemv_ternary_dequant(A, packed, scales, alpha, y=None, y_dtype=None, str
 def _here(t) -> int:
     """The device of t, which must be the current one (the kernels run there and take raw pointers)."""
     dev = t.get_device()
-    if dev != _torch().cuda.current_device():
+    if dev < 0 or dev != _torch().cuda.current_device():
         raise ValueError("tensors must be on the current CUDA device, got %s" % t.device)
     return dev
 
@@ -485,6 +485,15 @@ def _demand(dev: int, *wanted):
             raise ValueError("%s must be contiguous" % name)
 
 
+def _demand_line(dev: int, dtype, *wanted):
+    """Each (name, tensor, n): n contiguous values of the dtype on device dev (whatever their shape is called)."""
+    for name, t, n in wanted:
+        if t.numel() != n or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+            raise (TypeError if t.dtype is not dtype else ValueError)(
+                "%s: expected %d contiguous values of %s on CUDA device %d, got %s of %s on %s"
+                % (name, n, dtype, dev, tuple(t.shape), t.dtype, t.device))
+
+
 def _head_rows(name, t, dev: int) -> int:
     """Rows of heads [T][H][D], heads and values contiguous, any row stride (columns of a wider matrix): the stride."""
     if t.dim() != 3:
@@ -503,8 +512,9 @@ def _cache_shape(dev: int, k_codes, k_scales, v_codes, v_scales):
         raise ValueError("k_codes must be [blocks][heads][block][head dimension]")
     shape = k_codes.shape
     n, H, block, D = shape
-    _demand(dev, ("k_codes", k_codes, torch.uint8, shape), ("v_codes", v_codes, torch.uint8, shape),
-            ("k_scales", k_scales, torch.float32, (n, H)), ("v_scales", v_scales, torch.float32, (n, H)))
+    _demand(dev, ("v_codes", v_codes, torch.uint8, shape))
+    _demand_line(dev, torch.uint8, ("k_codes", k_codes, k_codes.numel()))
+    _demand_line(dev, torch.float32, ("k_scales", k_scales, n * H), ("v_scales", v_scales, n * H))
     return n, H, block, D
 
 
@@ -522,11 +532,10 @@ def hbl_kv_plan(cached, added, free_blocks, taken, table, block: int, T: int, to
     slots = new(T) if slots is None else slots
     positions = new(T) if positions is None else positions
     taken_out = new(1) if taken_out is None else taken_out
-    one, free = (B,), free_blocks.numel()
-    _demand(dev, ("table", table, i32, (B, width)), ("cached", cached, i32, one), ("added", added, i32, one),
-            ("free_blocks", free_blocks, i32, (free,)), ("taken", taken, i32, (1,)), ("total", total, i32, one),
-            ("row_start", row_start, i32, (B + 1,)), ("slots", slots, i32, (T,)), ("positions", positions, i32, (T,)),
-            ("taken_out", taken_out, i32, (1,)))
+    free = free_blocks.numel()
+    _demand_line(dev, i32, ("table", table, B * width), ("cached", cached, B), ("added", added, B),
+                 ("free_blocks", free_blocks, free), ("taken", taken, 1), ("total", total, B), ("row_start", row_start, B + 1),
+                 ("slots", slots, T), ("positions", positions, T), ("taken_out", taken_out, 1))
     _check(lib().hbl_kv_plan(cached.data_ptr(), added.data_ptr(), B, block, free_blocks.data_ptr(), free,
                              taken.data_ptr(), table.data_ptr(), width, T, total.data_ptr(), row_start.data_ptr(),
                              slots.data_ptr(), positions.data_ptr(), taken_out.data_ptr(), _raw_stream(stream, dev)),
@@ -545,7 +554,7 @@ def hbl_kv_append(k, v, slots, k_codes, k_scales, v_codes, v_scales, bits: int =
         raise ValueError("k and v: expected shape %s, got %s and %s" % ((T, H, D), tuple(k.shape), tuple(v.shape)))
     if v.dtype is not k.dtype:
         raise TypeError("k and v must have one dtype, got %s and %s" % (k.dtype, v.dtype))
-    _demand(dev, ("slots", slots, _torch().int32, (T,)))
+    _demand_line(dev, _torch().int32, ("slots", slots, T))
     _check(lib().hbl_kv_append(k.data_ptr(), v.data_ptr(), _dtype_code(k), T, H, D, ks, vs, slots.data_ptr(), bits, n,
                                block, k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
                                _raw_stream(stream, dev)), "hbl_kv_append")
@@ -574,10 +583,11 @@ def hbl_kv_attention(q, row_start, total, table, k_codes, k_scales, v_codes, v_s
         o = torch.zeros((T, Hq, D), dtype=o_dtype or q.dtype, device=q.device)
     if workspace is None:
         workspace = torch.empty((hbl_kv_attention_workspace_bytes(T, Hq, Hkv, D, B),), dtype=torch.uint8, device=q.device)
-    _demand(dev, ("row_start", row_start, i32, (B + 1,)), ("total", total, i32, (B,)), ("table", table, i32, (B, width)),
-            ("o", o, None, (T, Hq, D)), ("workspace", workspace, None, workspace.shape))
+    _demand_line(dev, i32, ("row_start", row_start, B + 1), ("total", total, B), ("table", table, B * width))
+    _demand_line(dev, workspace.dtype, ("workspace", workspace, workspace.numel()))
+    _demand(dev, ("o", o, None, (T, Hq, D)))
     if scale is not None:
-        _demand(dev, ("scale", scale, torch.float32, (1,)))
+        _demand_line(dev, torch.float32, ("scale", scale, 1))
     _check(lib().hbl_kv_attention(q.data_ptr(), _dtype_code(q), T, qs, Hq, Hkv, D, row_start.data_ptr(), total.data_ptr(),
                                   B, table.data_ptr(), width, n, block, bits, k_codes.data_ptr(), k_scales.data_ptr(),
                                   v_codes.data_ptr(), v_scales.data_ptr(), None if scale is None else scale.data_ptr(),
@@ -596,20 +606,22 @@ def hbl_add_rms_quant(x, bits: int, residual=None, gain=None, h=None, codes=None
     """h = x + residual, then RMSNorm with a float32 gain [K] and the per-token quantizer (bits 8 absmax, 4 absmean):
     (h [M][K] of x's dtype, int8 codes [M][K], float32 scales [M]).  h may be x or residual itself."""
     torch = _torch()
-    dev, dtype, shape = _here(x), x.dtype, x.shape
-    M, K = shape
+    dev, dtype = _here(x), x.dtype
+    M, K = x.shape
     if h is None:
         h = torch.empty_like(x)
     if codes is None:
         codes = torch.empty((M, K), dtype=torch.int8, device=x.device)
     if scales is None:
         scales = torch.empty((M,), dtype=torch.float32, device=x.device)
-    _demand(dev, ("x", x, dtype, shape), ("h", h, dtype, shape), ("codes", codes, torch.int8, shape),
-            ("scales", scales, torch.float32, (M,)))
+    n = M * K
+    _demand_line(dev, dtype, ("x", x, n), ("h", h, n))
+    _demand_line(dev, torch.int8, ("codes", codes, n))
+    _demand_line(dev, torch.float32, ("scales", scales, M))
     if residual is not None:
-        _demand(dev, ("residual", residual, dtype, shape))
+        _demand_line(dev, dtype, ("residual", residual, n))
     if gain is not None:
-        _demand(dev, ("gain", gain, torch.float32, (K,)))
+        _demand_line(dev, torch.float32, ("gain", gain, K))
     _check(lib().hbl_add_rms_quant(x.data_ptr(), _opt(residual), _dtype_code(x), M, K, _opt(gain), bits, h.data_ptr(),
                                    codes.data_ptr(), scales.data_ptr(), _raw_stream(stream, dev)), "hbl_add_rms_quant")
     return h, codes, scales
@@ -624,21 +636,23 @@ def hbl_add_rms_quant_backward(h, g_t, gain=None, g_h=None, g_x=None, g_gain=Non
     (h's dtype) along the residual stream.  Returns (g_x [M][K] of h's dtype, for x and residual alike; g_gain
     float32 [K], None without a gain)."""
     torch = _torch()
-    dev, dtype, shape, f32 = _here(h), h.dtype, h.shape, torch.float32
-    M, K = shape
+    dev, dtype, f32 = _here(h), h.dtype, torch.float32
+    M, K = h.shape
     if g_x is None:
         g_x = torch.empty_like(h)
     if g_gain is None and gain is not None:
         g_gain = torch.empty((K,), dtype=f32, device=h.device)
     if workspace is None:
         workspace = torch.empty((hbl_add_rms_quant_backward_workspace_bytes(M, K),), dtype=torch.uint8, device=h.device)
-    _demand(dev, ("h", h, dtype, shape), ("g_t", g_t, None, shape), ("g_x", g_x, dtype, shape),
-            ("workspace", workspace, None, workspace.shape))
+    n = M * K
+    _demand_line(dev, dtype, ("h", h, n), ("g_x", g_x, n))
+    _demand_line(dev, g_t.dtype, ("g_t", g_t, n))
+    _demand_line(dev, workspace.dtype, ("workspace", workspace, workspace.numel()))
     if g_h is not None:
-        _demand(dev, ("g_h", g_h, dtype, shape))
+        _demand_line(dev, dtype, ("g_h", g_h, n))
     for name, t in (("gain", gain), ("g_gain", g_gain)):
         if t is not None:
-            _demand(dev, (name, t, f32, (K,)))
+            _demand_line(dev, f32, (name, t, K))
     _check(lib().hbl_add_rms_quant_backward(h.data_ptr(), _dtype_code(h), M, K, _opt(gain), g_t.data_ptr(),
                                             _dtype_code(g_t), _opt(g_h), g_x.data_ptr(), _opt(g_gain),
                                             workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, dev)),
