@@ -406,7 +406,8 @@ size_t hbl_kv_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t Hkv, int6
  *   o          device, [T][Hq][D] of dtype ot
  *   workspace  device, 256-byte aligned, >= hbl_kv_attention_workspace_bytes
  *              bytes; scratch, of one call at a time
- * Hq a multiple of Hkv, Hq <= 1024, T * Hq below 2^31.  Scores, softmax sums and outputs are
+ * Hq a multiple of Hkv, Hq <= 1024, T * Hq below 2^31, width * block at
+ * most 2^31 - 256.  Scores, softmax sums and outputs are
  * accumulated in float; codes enter the products exactly; queries (scaled by a
  * power of two per row) and weights enter them as fp16, in two parts when q is
  * HBL_F32, so its products carry 22 bits. */

@@ -570,6 +570,7 @@ hbl_status hbl_kv_attention(const void* q, hbl_dtype qt, int64_t T, int64_t q_st
   if ((s = check_requests(B, width)) != HBL_OK) return s;
   if (T * Hq > INT32_MAX) return HBL_ERR_UNSUPPORTED;  // rows of a request are counted in 32 bits
   if ((s = check_cache(num_blocks, block, bits)) != HBL_OK) return s;
+  if (width > (INT32_MAX - 255) / block) return HBL_ERR_UNSUPPORTED;  // and so are its tokens, a tile past the last
   if ((s = check_row_stride(q_stride, Hq, D, qt)) != HBL_OK) return s;
   if (!workspace || !aligned(workspace, 256) ||
       workspace_bytes < hbl_kv_attention_workspace_bytes(T, Hq, Hkv, D, B))

@@ -84,18 +84,21 @@ __device__ __forceinline__ Request request_of(const KvAttentionArgs& a, int b, i
   return r;
 }
 
-// Prefix sums of the requests' tiles in shared memory, by the whole CTA.
-__device__ __forceinline__ int64_t lay_line(const KvAttentionArgs& a, int rows_per_tile, int64_t* start,
-                                            int64_t* warp_sums) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (a.B + kThreads - 1) / kThreads;
-  const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
-  int64_t s = 0;
-  for (int b = b0; b < b1; ++b) {
-    const Request r = request_of(a, b, rows_per_tile);
-    start[b] = s;
-    s += r.tiles * r.items;
+// How the line of tiles is shared out: a warp takes `per` places of it.  Where
+// the items are few beside the warps, each begins a share of its own (`pitch`
+// places of the line, a multiple of per, for its tiles): a warp that went on
+// from one item to the next would take twice as long as the others.
+struct Line {
+  int64_t units, per;
+  bool padded;
+  __device__ __forceinline__ int64_t pitch(const Request& r) const {
+    return padded ? (r.tiles + per - 1) / per * per : r.tiles;
   }
+};
+
+// Sum over the CTA of s, and what lies before this thread's.
+__device__ __forceinline__ int64_t scan(int64_t s, int64_t* warp_sums, int64_t& before) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t inc = s;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -104,15 +107,48 @@ __device__ __forceinline__ int64_t lay_line(const KvAttentionArgs& a, int rows_p
   }
   if (lane == 31) warp_sums[warp] = inc;
   __syncthreads();
-  int64_t base = inc - s, all = 0;
+  before = inc - s;
+  int64_t all = 0;
+#pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) base += warp_sums[w];
+    if (w < warp) before += warp_sums[w];
     all += warp_sums[w];
   }
-  for (int b = b0; b < b1; ++b) start[b] += base;
-  if (tid == 0) start[a.B] = all;
-  __syncthreads();
   return all;
+}
+
+// Prefix sums of the requests' places in shared memory, by the whole CTA.
+__device__ __forceinline__ Line lay_line(const KvAttentionArgs& a, int rows_per_tile, int64_t workers, int64_t* start,
+                                         int64_t (*warp_sums)[kWarps]) {
+  const int tid = threadIdx.x;
+  const int each = (a.B + kThreads - 1) / kThreads;
+  const int b0 = min(tid * each, a.B), b1 = min(b0 + each, a.B);
+  int64_t tiles = 0, items = 0, before, unused;
+  for (int b = b0; b < b1; ++b) {
+    const Request r = request_of(a, b, rows_per_tile);
+    start[b] = tiles;
+    tiles += r.tiles * r.items;
+    items += r.items;
+  }
+  Line line;
+  line.units = scan(tiles, warp_sums[0], before);
+  items = scan(items, warp_sums[1], unused);
+  line.padded = items <= workers / 4;
+  const int64_t shares = line.padded ? workers - items : workers;  // of `per` places: an item's last one may not be full
+  line.per = max((line.units + shares - 1) / shares, (int64_t)kMinTiles);
+  if (line.padded) {
+    tiles = 0;
+    for (int b = b0; b < b1; ++b) {
+      const Request r = request_of(a, b, rows_per_tile);
+      start[b] = tiles;
+      tiles += line.pitch(r) * r.items;
+    }
+    line.units = scan(tiles, warp_sums[2], before);
+  }
+  for (int b = b0; b < b1; ++b) start[b] += before;
+  if (tid == 0) start[a.B] = line.units;
+  __syncthreads();
+  return line;
 }
 
 // the request of a place in the line (start rising; equal starts: the last,
@@ -386,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, NT, F32)) kv_attent
   constexpr int kRows = 8 * NT;
   constexpr int kCopies = kHalf >= 512 ? kHalf / 512 : 1;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t warp_sums[kWarps];
+  __shared__ int64_t warp_sums[3][kWarps];
   __shared__ float2 cta_ml[kWarps][kRows];
   int64_t* start = reinterpret_cast<int64_t*>(smem + kWarps * kStages * kStage);
 
@@ -396,8 +432,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, NT, F32)) kv_attent
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   const int64_t workers = (int64_t)gridDim.x * kWarps;
-  const int64_t units = lay_line(a, kRows, start, warp_sums);
-  const int64_t per = max((units + workers - 1) / workers, (int64_t)kMinTiles);
+  const Line line = lay_line(a, kRows, workers, start, warp_sums);
+  const int64_t units = line.units, per = line.per;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane & 3, gid = lane >> 2;
   const int64_t worker = (int64_t)blockIdx.x * kWarps + warp;
   int64_t u = worker * per;
@@ -414,9 +450,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, NT, F32)) kv_attent
   bool alone = false;
   if (c0 < c1) {
     const int b = find_request(start, a.B, c0);
-    const int tiles = request_of(a, b, kRows).tiles;
-    const int64_t end = start[b] + ((c0 - start[b]) / tiles + 1) * tiles;
-    alone = c1 <= end;
+    const int64_t pitch = line.pitch(request_of(a, b, kRows));
+    alone = c1 <= start[b] + ((c0 - start[b]) / pitch + 1) * pitch;
   }
   if ((u >= u_end || (alone && warp != 0)) && lane == 0) {
     Record& rec = parts.record[worker];
@@ -432,14 +467,14 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, NT, F32)) kv_attent
   while (u < u_end) {
     const int b = find_request(start, a.B, u);
     const Request r = request_of(a, b, kRows);
-    const int64_t in_request = u - start[b];
-    const int64_t item = in_request / r.tiles;
-    const int t0 = (int)(in_request - item * r.tiles);            // first tile of the item here
+    const int64_t in_request = u - start[b], pitch = line.pitch(r);
+    const int64_t item = in_request / pitch;
+    const int t0 = (int)(in_request - item * pitch);              // first tile of the item here
     const int t1 = (int)min((int64_t)r.tiles, t0 + (u_end - u));  // end of the tiles here
     const int row_tile = (int)(item / a.Hkv), row0 = row_tile * kRows;
     const int h = (int)(item - (int64_t)row_tile * a.Hkv);
     const int64_t i0 = u - t0;
-    u += t1 - t0;
+    u = line.padded ? u_end : u + (t1 - t0);
 
     // tokens that the tile's first and last row see, and tiles to work on (none: n <= 0)
     const int all_see = min(r.pos0 + row0 / g + 1, r.keys);
@@ -741,7 +776,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, NT, F32)) kv_attent
         const int64_t i1 = i0 + r.tiles, w1 = (i1 - 1) / per, share = kWarps * per;
         const int64_t first_cta = blockIdx.x;
         rec.last_cta = w1 / kWarps;
-        const bool last_in = rec.last_cta * share >= i0 && min((rec.last_cta + 1) * share, units) <= i1;
+        const bool last_in = rec.last_cta * share >= i0 && min((rec.last_cta + 1) * share, units) <= i0 + pitch;
         rec.head = alone ? 0 : (int)(min(w1, first_cta * kWarps + kWarps - 1) - worker + 1);
         rec.mid_cta = alone ? first_cta : first_cta + 1;
         rec.mid = (int)max((last_in ? rec.last_cta : rec.last_cta - 1) - rec.mid_cta + 1, (int64_t)0);
@@ -770,11 +805,16 @@ __global__ void __launch_bounds__(kJoinThreads) kv_attention_join_kernel(const K
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = a.Hq / a.Hkv;
   int dealt = 0;  // rows dealt out to the warps so far
+  int counts = 0;  // of the record that a lane looks at: all at once, most are empty
+  if (lane < kWarps) {
+    const Record& rec = parts.record[(int64_t)blockIdx.x * kWarps + lane];
+    counts = rec.head + rec.mid + rec.tail;
+  }
   for (int own = 0; own < kWarps; ++own) {
     const int64_t w0 = (int64_t)blockIdx.x * kWarps + own;
-    const Record rec = parts.record[w0];
-    const int count = rec.head + rec.mid + rec.tail;
+    const int count = __shfl_sync(0xffffffffu, counts, own);
     if (count == 0) continue;
+    const Record rec = parts.record[w0];
     for (int y = (warp - dealt) & (kJoinThreads / 32 - 1); y < rec.rows; y += kJoinThreads / 32) {
       auto slot = [&](int p) {
         const int64_t w = p < rec.head ? w0 + p

@@ -64,7 +64,7 @@ def test_kv_attention_refusals(L):
     _refuses(f, good, [(i, ODD, E_ARG) for i in (0, 7, 8, 10, 15, 16, 17, 18, 19, 20)])
     _refuses(f, good, [(1, 2, E_ARG), (21, 2, E_ARG), (2, 0, E_ARG), (3, 4095, E_ARG), (3, 4100, E_ARG), (4, 0, E_ARG),
                        (4, 30, E_UNS), (4, 2048, E_UNS), (5, 0, E_ARG), (6, 0, E_ARG), (6, 80, E_UNS), (9, 0, E_ARG),
-                       (9, 4097, E_UNS), (11, 0, E_ARG), (12, 0, E_ARG), (12, 1 << 25, E_UNS), (13, 0, E_ARG),
+                       (9, 4097, E_UNS), (11, 0, E_ARG), (11, 1 << 25, E_UNS), (2, 1 << 26, E_UNS), (12, 0, E_ARG), (12, 1 << 25, E_UNS), (13, 0, E_ARG),
                        (13, 24, E_UNS), (14, 0, E_ARG), (14, 1, E_UNS), (14, 9, E_UNS), (20, A, E_ARG),
                        (22, NULL, E_WS), (22, ctypes.c_void_p(0x30010), E_WS), (23, ws - 1, E_WS)])
     for bad in ((0, 32, 8, 128, 4), (8, 32, 5, 128, 4), (8, 32, 8, 100, 4), (8, 32, 8, 128, 0), (8, 32, 8, 128, 5000)):
