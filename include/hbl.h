@@ -344,8 +344,8 @@ hbl_status hbl_kv_quant(const void* x, hbl_dtype xt, int64_t rows, int64_t D, in
  *   cached       device, [B]: tokens each request has in the cache
  *   added        device, [B]: token rows it brings in this step (0 allowed)
  *   B            requests, 1 .. 4096
- *   free_blocks  device, [num_free]: ids of blocks nobody owns; the step takes
- *                them in order from place taken[0] on
+ *   free_blocks  device, [num_free]: ids of blocks nobody owns (NULL for none);
+ *                the step takes them in order from place taken[0] on
  *   table        device, [B][width], updated in place: entries of blocks that
  *                a request did not have yet are written, no others; blocks
  *                past `width` are not given out

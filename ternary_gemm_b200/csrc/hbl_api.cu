@@ -505,8 +505,8 @@ hbl_status hbl_kv_plan(const int32_t* cached, const int32_t* added, int64_t B, i
                        const int32_t* free_blocks, int64_t num_free, const int32_t* taken, int32_t* table,
                        int64_t width, int64_t T, int32_t* total, int32_t* row_start, int32_t* slots,
                        int32_t* positions, int32_t* taken_out, cudaStream_t stream) {
-  if (!cached || !added || !free_blocks || !taken || !table || !total || !row_start || !slots || !positions ||
-      !taken_out || num_free < 0)
+  if (!cached || !added || (!free_blocks && num_free != 0) || !taken || !table || !total || !row_start || !slots ||
+      !positions || !taken_out || num_free < 0)
     return HBL_ERR_INVALID_ARG;
   for (const void* p : {(const void*)cached, (const void*)added, (const void*)free_blocks, (const void*)taken,
                         (const void*)table, (const void*)total, (const void*)row_start, (const void*)slots,

@@ -99,6 +99,18 @@ def test_plan_short_of_rows_blocks_and_width(H):
             assert np.array_equal(to_host(g).reshape(-1), np.asarray(w).reshape(-1))
 
 
+def test_plan_without_free_blocks(H):
+    """Steps that need no block take an empty free list; one that needs some gets -1."""
+    import torch
+    table = _i32([[5, -1], [2, 3]])
+    none = torch.empty((0,), dtype=torch.int32, device="cuda")
+    for cached, added in (([3, 17], [2, 15]), ([16, 20], [1, 1])):
+        want = ref.plan(cached, added, [], 0, to_host(table), 16, 20)
+        got = H.hbl_kv_plan(_i32(cached), _i32(added), none, _i32([0]), table, 16, 20)
+        for g, w in zip((table,) + got, want):
+            assert np.array_equal(to_host(g).reshape(-1), np.asarray(w).reshape(-1))
+
+
 # ------------------------------------------------------------------ append
 
 def _cache(rng, n, H, block, D, bits):
@@ -400,6 +412,92 @@ def test_attention_long(H):
                                       ref.values(small_v, small_vs, 8), D ** -0.5)
     tol = ref.attention_tolerance(want, *sizes, 20000, False, False)
     assert np.all(np.abs(got - want) <= tol)
+
+
+@pytest.mark.parametrize("B,new", [(1500, 1), (4096, 1), (600, 9)])
+def test_attention_many_requests(H, B, new):
+    rng = np.random.default_rng(B)
+    total = rng.integers(0, 70, B)
+    rows = rng.integers(0, new + 1, B)
+    rows[0] = new
+    _attend(H, rng, rows.tolist(), total, 2, 1, 64, 16, 8, True)
+
+
+def test_attention_over_shared_and_repeated_blocks(H):
+    """One block in several requests' tables, and twice in one: a shared prefix, read by all."""
+    def mend(table, kc, ks, vc, vs, q):
+        table[1, :4] = table[0, :4]
+        table[2, 1] = table[2, 0]
+    for new in ([1, 1, 1], [90, 120, 64]):
+        _attend(H, np.random.default_rng(sum(new)), new, np.array([130, 150, 140]), 8, 2, 128, 16, 8, True, mend=mend)
+
+
+def test_prompt_attention_in_a_graph(H):
+    """Chunks of prompts, captured once and replayed with other lengths, rows and pages (the same batch size)."""
+    import torch
+    rng = np.random.default_rng(31)
+    Hq, Hkv, D, block, n, T = 16, 4, 128, 32, 400, 700
+    cache = [_dev(a) for a in _cache(rng, n, Hkv, block, D, 8) + _cache(rng, n, Hkv, block, D, 8)]
+    q, o = _as(rng.standard_normal((T, Hq, D)), True), torch.zeros((T, Hq, D), dtype=torch.bfloat16, device="cuda")
+    rows, total, table = _i32([0, 300, 700]), _i32([2000, 900]), _i32(rng.integers(0, n, (2, 90)))
+    ws = torch.empty((H.hbl_kv_attention_workspace_bytes(T, Hq, Hkv, D, 2),), dtype=torch.uint8, device="cuda")
+    call = lambda out, w: H.hbl_kv_attention(q, rows, total, table, *cache, o=out, workspace=w)  # noqa: E731
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        call(o, ws)
+    stream.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        call(o, ws)
+    other = torch.empty_like(ws)
+    for r, t in (([0, 300, 700], [2000, 900]), ([0, 64, 65], [64, 2500]), ([0, 0, 690], [5, 2800]), ([10, 500, 700], [490, 200])):
+        rows.copy_(_i32(r))
+        total.copy_(_i32(t))
+        table.copy_(_i32(rng.integers(-3, n + 3, (2, 90))))
+        q.copy_(_as(rng.standard_normal((T, Hq, D)), True))
+        want = torch.full_like(o, 3.0)
+        o.fill_(3.0)
+        call(want, other)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, want)
+        ref_o, *sizes = ref.attention(_np(q), r, t, to_host(table), ref.values(to_host(cache[0]), to_host(cache[1]), 8),
+                                      ref.values(to_host(cache[2]), to_host(cache[3]), 8), D ** -0.5, to_host(cache[3]))
+        mine = ~np.isnan(ref_o[:, 0, 0])
+        tol = ref.attention_tolerance(ref_o, *sizes, max(t), False, False)
+        assert np.all(np.abs(_np(o) - ref_o)[mine] <= tol[mine]) and np.all(_np(o)[~mine] == 3.0)
+    assert H.hbl_last_device_error() == H.HBL_OK
+
+
+def test_prompt_attention_on_two_streams(H):
+    """Two prompts at once (each wants all of an SM's tensor memory) with workspaces of their own, beside a product
+    that uses tensor memory too."""
+    import torch
+    rng = np.random.default_rng(32)
+    Hq, Hkv, D, n = 16, 4, 128, 300
+    cache = [_dev(a) for a in _cache(rng, n, Hkv, 64, D, 8) + _cache(rng, n, Hkv, 64, D, 8)]
+    args = (_i32([0, 900]), _i32([4000]), _i32(rng.permutation(n)[:64].reshape(1, 64)), *cache)
+    qs = [_as(rng.standard_normal((900, Hq, D)), True) for _ in range(2)]
+    want = [H.hbl_kv_attention(q, *args) for q in qs]
+    A, W = (torch.randint(-8, 8, s, device="cuda", dtype=torch.int8) for s in ((512, 2048), (1024, 2048)))
+    acc = H.hbl_gemm_i8_i32(A, W)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    size = H.hbl_kv_attention_workspace_bytes(900, Hq, Hkv, D, 1)
+    ws = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    outs = [[torch.zeros_like(want[0]) for _ in range(4)] for _ in range(2)]
+    accs = [torch.zeros_like(acc) for _ in range(4)]
+    torch.cuda.synchronize()
+    for i in range(4):
+        for j in (0, 1):
+            with torch.cuda.stream(streams[j]):
+                H.hbl_kv_attention(qs[j], *args, o=outs[j][i], workspace=ws[j])
+        with torch.cuda.stream(streams[2]):
+            H.hbl_gemm_i8_i32(A, W, acc=accs[i])
+    torch.cuda.synchronize()
+    for i in range(4):
+        assert torch.equal(outs[0][i], want[0]) and torch.equal(outs[1][i], want[1]) and torch.equal(accs[i], acc)
+    assert H.hbl_last_device_error() == H.HBL_OK
 
 
 def test_attention_is_reproducible(H):
