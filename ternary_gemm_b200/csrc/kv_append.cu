@@ -250,10 +250,10 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 6 : 5) kv_append_kernel(const
 }  // namespace
 
 cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t stream) {
-  // Rows per CTA, then heads: as many as leave about sixteen CTAs per SM, so
+  // Rows per CTA, then heads: as many as leave about thirty CTAs per SM, so
   // that a decode batch has one row and head a CTA, and a prompt shares the
   // search for its runs among several heads.
-  const int64_t ctas = a.T * a.H * 2, want = (int64_t)sm100_host::sm_count() * 16;
+  const int64_t ctas = a.T * a.H * 2, want = (int64_t)sm100_host::sm_count() * 32;
   int group = 1, span = 1;
   while (group < kMaxGroup && ctas / (group * 2) >= want) group *= 2;
   while (span < kMaxSpan && ctas / ((int64_t)group * span * 2) >= want) span *= 2;

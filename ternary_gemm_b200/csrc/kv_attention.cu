@@ -51,14 +51,16 @@ constexpr float kLog2e = 1.4426950408889634f;
 // a warp takes at least this many tiles of the line
 constexpr int kMinTiles = 2;
 
-// Blocks per SM and stages per warp: copies in flight (about 100 KB on an SM)
+// Blocks per SM and stages per warp: copies in flight (over 100 KB on an SM)
 // and warps enough to hide the products' latency, at the registers that the
-// accumulators (4 NT D / 16 per thread) and the queries leave.
+// accumulators (4 NT D / 16 per thread) and the queries leave.  At D = 128 two
+// blocks with two tiles ahead took 77 us where three with one ahead took 80
+// (two requests of 131072 tokens), and 23 against 25 (one of 32768).
 __host__ __device__ constexpr int blocks_per_sm(int D, int NT, bool f32) {
   const int weight = D * NT * (f32 ? 3 : 2);   // registers go with accumulators and query parts
-  return weight <= 128 ? 4 : (weight <= 384 ? 3 : (weight <= 768 && D < 256 ? 2 : 1));
+  return D == 256 ? 1 : (D == 128 ? 2 : (weight <= 128 ? 4 : 3));
 }
-__host__ __device__ constexpr int stages_of(int D) { return D >= 128 ? 2 : (D == 64 ? 3 : 6); }
+__host__ __device__ constexpr int stages_of(int D) { return D == 256 ? 2 : (D >= 64 ? 3 : 6); }
 
 // Rows, tiles per row tile, and row tiles of a request.
 struct Request {
