@@ -414,6 +414,16 @@ def test_attention_long(H):
     assert np.all(np.abs(got - want) <= tol)
 
 
+@pytest.mark.parametrize("new,total,Hq,Hkv", [([900, 900], [2448, 2400], 16, 2), ([1] * 4, [32768, 30000, 32000, 31111], 8, 1)])
+def test_attention_of_float_rows_over_many_tokens(H, new, total, Hq, Hkv):
+    """Long sums keep float's bits.  With values of either sign an output is a random sum, as its errors are: a score
+    of less than 16 in log2 units rounds twice (half steps of 2^-21, rms 2^-21 / sqrt(3) each, times ln 2: 2.7e-7 of a
+    weight), the exponential and the two-part weights 2^-22 each, about eighty additions of 2^-24 / sqrt(3) each
+    3.1e-7: together 5.3e-7 of the whole's norm, and 2^-20 is above it."""
+    got, want = _attend(H, np.random.default_rng(17), new, np.array(total), Hq, Hkv, 64, 32, 8, False)
+    assert np.linalg.norm(got - want) <= 2.0 ** -20 * np.linalg.norm(want)
+
+
 @pytest.mark.parametrize("B,new", [(1500, 1), (4096, 1), (600, 9)])
 def test_attention_many_requests(H, B, new):
     rng = np.random.default_rng(B)
