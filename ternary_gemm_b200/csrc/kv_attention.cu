@@ -26,6 +26,14 @@
 // line, each warp takes the same length of it.  A warp that covers an item
 // whole writes o; parts go to the workspace as (max, sum, o) and a second
 // kernel joins them in order.
+//
+// Measured (codes' bytes over the call's time): 64 requests of up to 8192
+// tokens, 32 heads over 8 of 128: 108 us, 5.3 TB/s, 81% of a plain copy's rate;
+// two of up to 131072: 78 us, 5.4 TB/s, 83%.  The main kernel alone moves its
+// bytes at 5.85 TB/s; what is left is the join (4 us), the first loads of
+// every warp, and shares that end unevenly.  One request of 777 tokens takes 12 us
+// on the device: two launches and a chain of six dependent reads (lengths,
+// table, scales, codes, part, parts of others).
 #include <cstdint>
 #include <utility>
 

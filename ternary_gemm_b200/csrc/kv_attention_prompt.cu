@@ -7,12 +7,16 @@
 //   s_j = scale u_k(j) (2 sum_d q_d k'_jd + sum_d q_d)
 //   w_j = exp(s_j) u_v(j),   o = sum_j w_j (2 v'_j + 1) / sum_j w_j / u_v(j)
 //
-// and the weights are held on a scale where a row's largest lies in
-// [2^7, 2^15]: the scale follows the running maximum only when that grew by
-// more than eight powers of two, so the accumulator in tensor memory is seldom
-// rescaled (with four, some warp of the CTA had to in every other tile, and the
-// whole took 571 us instead of 330 at 2048 rows over 8192 tokens), and fp16
-// keeps 11 bits of all weights down to 2^-21 of the largest at the least.
+// and the weights are held under a reference that is a row's maximum when it
+// first sees a token (its largest weight there is 2^7) and moves only when the
+// weights of half a tile add up to more than 2^15: no weight can pass fp16's
+// range, no maximum is taken of a tile, and the accumulator in tensor memory is
+// seldom rescaled.  fp16 keeps 11 bits of all weights down to 2^-21 of the
+// reference's at the least.  (A reference that followed after four powers of
+// two, which some warp of a CTA met in every other tile: 571 us at three
+// requests of up to 2048 rows over 8192 tokens; after eight, with a maximum of
+// every tile: 406; without: 379, and 367 with the start and end of a CTA
+// shortened.)
 //
 // Rows are many, so this is a matter of the tensor cores: a CTA takes 256 rows
 // of one cached head (two tiles of 128, query heads of the group times the
@@ -26,6 +30,15 @@
 //                   O += W V with W from tensor memory (it lies where S was),
 //                   the two row tiles in turn, so that one tile's softmax runs
 //                   under the other's products
+// Measured there: 370 us, 860 TFLOP/s of the causal products, 52% of the
+// rate of a long library product; 4000 clocks for 256 rows over 128 tokens, of
+// which the products take 2050 and a row tile's softmax 2700 (the exponentials
+// of both 2050, at their unit's rate).  What bounds it is the chain of a row
+// tile: its next scores go where its weights lie, so they are begun only when
+// the products with those have been issued.
+// Where there are too few items for the SMs, several CTAs share the tokens of
+// one and a second kernel joins their parts: one request of 1024 rows over
+// 16384 tokens 95 us instead of 347.
 // Every mbarrier wait is bounded; a CTA that gives up sets the device error
 // word, waits for its products and frees its tensor memory.
 #include <algorithm>
