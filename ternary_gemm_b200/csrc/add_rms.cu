@@ -20,8 +20,8 @@
 // kernel in fixed order.
 //
 // Measured at 8192 bf16 rows of 4096: forward 42 us, 5.6 TB/s, 85% of a plain
-// copy's rate; gradient 54 us, 5.0 TB/s, 75% (46 of them the rows, the rest the
-// sum over CTAs and its launch).  One row of 2560: 3.3 us on the device.
+// copy's rate; gradient 49 us, 5.5 TB/s, 83% (about 45 of them the rows, the
+// rest the sum over CTAs and its launch).  One row of 2560: 3.3 us on the device.
 #include <cstdint>
 
 #include "common.cuh"
@@ -276,10 +276,21 @@ add_rms_quant_kernel(const void* x, const void* residual, int64_t M, int K, cons
 
 // ---------------------------------------------------------------- gradient
 
+// B blocks of an SM as one, which leaves one row of partial sums instead of B
+// (592 of them took 8 us to add up at 4096 columns).
+template <typename S, int B>
+struct Wide {
+  static constexpr int T = S::T, E = S::E;
+  static constexpr int kThreads = B * S::kThreads;
+  static constexpr int R = B * S::R;
+  static constexpr int kWarpsPerRow = S::kWarpsPerRow;
+};
+
 // A grid that stays: a thread's columns of the gain's sums stay in registers
-// over its rows.  kStages as above (three tensors a row).
-template <typename S, bool BF16, bool GT16, int kStages, int kBlocks>
-__global__ void __launch_bounds__(S::kThreads, kBlocks)
+// over its rows.  kStages as above (three tensors a row).  Row r goes to CTA
+// r mod grid, so that few rows still take many SMs.
+template <typename S, bool BF16, bool GT16, int kStages>
+__global__ void __launch_bounds__(S::kThreads, most_blocks(S::kThreads))
 add_rms_grad_kernel(const void* __restrict__ h, int64_t M, int K, const float* __restrict__ gain,
                     const void* __restrict__ g_t, const void* g_h, void* g_x, float* __restrict__ sums) {
   constexpr int T = S::T, E = S::E, WPR = S::kWarpsPerRow;
@@ -291,7 +302,7 @@ add_rms_grad_kernel(const void* __restrict__ h, int64_t M, int K, const float* _
   const int rl = threadIdx.x / T, t = threadIdx.x % T;
   const int vectors = K / 8;
   const float inv_k = __fdiv_rn(1.0f, (float)K);
-  const int64_t step = (int64_t)gridDim.x * S::R;
+  const int64_t grid = gridDim.x, step = grid * S::R;
   const uint32_t ring = sm100::smem_u32(ring_bytes);
   float acc[E][8], w[kGain ? E : 1][8];
 #pragma unroll
@@ -314,7 +325,7 @@ add_rms_grad_kernel(const void* __restrict__ h, int64_t M, int K, const float* _
     }
     cp_commit();
   };
-  int64_t row = (int64_t)blockIdx.x * S::R + rl;
+  int64_t row = blockIdx.x + rl * grid;
   uint32_t here = ring, next = ring;
   if constexpr (kRinged) {
 #pragma unroll
@@ -324,7 +335,7 @@ add_rms_grad_kernel(const void* __restrict__ h, int64_t M, int K, const float* _
     }
   }
   int parity = 0;
-  for (int64_t row0 = (int64_t)blockIdx.x * S::R; row0 < M; row0 += step, row += step, parity ^= 1) {
+  for (int64_t row0 = blockIdx.x; row0 < M; row0 += step, row += step, parity ^= 1) {
     const bool active = row < M;
     const int64_t base = (active ? row : 0) * K;
     if constexpr (kRinged) {
@@ -369,7 +380,7 @@ add_rms_grad_kernel(const void* __restrict__ h, int64_t M, int K, const float* _
     }
     if constexpr (T > 32) {
       if ((t & 31) == 0) red[parity][rl * WPR + (t >> 5)] = make_float2(ss, dot);
-      __syncthreads();
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + rl), "n"(T) : "memory");  // the row's threads
       ss = dot = 0.0f;
 #pragma unroll
       for (int i = 0; i < WPR; ++i) {
@@ -408,10 +419,38 @@ add_rms_grad_kernel(const void* __restrict__ h, int64_t M, int K, const float* _
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the sum over CTAs waits for the grid's end
   if (!sums) return;
+  sums += (int64_t)blockIdx.x * K;
+  if constexpr (S::R == 1) {
 #pragma unroll
-  for (int j = 0; j < E; ++j) {
-    const int i = j * T + t;
-    if (i < vectors) store8<false>(sums, ((int64_t)blockIdx.x * S::R + rl) * K + i * 8, acc[j]);
+    for (int j = 0; j < E; ++j) {
+      const int i = j * T + t;
+      if (i < vectors) store8<false>(sums, i * 8, acc[j]);
+    }
+  } else {
+    // the CTA's rows, in order, through the ring's memory
+    static_assert(kRinged && 2 * kRow >= S::R * T * E * 32, "the sums fit the ring");
+    float4* part = reinterpret_cast<float4*>(ring_bytes);  // [row][half of a vector][vector]
+    cp_wait<0>();
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      float4* to = part + rl * 2 * T * E + j * T + t;
+      to[0] = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
+      to[T * E] = make_float4(acc[j][4], acc[j][5], acc[j][6], acc[j][7]);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < vectors; i += S::kThreads) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        float4 s = part[half * T * E + i];
+#pragma unroll
+        for (int r = 1; r < S::R; ++r) {
+          const float4 v = part[(2 * r + half) * T * E + i];
+          s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+        }
+        reinterpret_cast<float4*>(sums)[2 * i + half] = s;
+      }
+    }
   }
 }
 
@@ -459,6 +498,12 @@ cudaError_t start(Kernel kernel, std::atomic<bool> (&done)[sm100_host::kMaxDevic
   return cudaGetLastError();
 }
 
+// CTAs of the gradient, and rows of partial sums of the gain's
+int64_t grad_grid(int64_t M, int blocks) {
+  const int64_t cap = (int64_t)sm100_host::sm_count() * blocks;
+  return M < cap ? M : cap;
+}
+
 template <typename S>
 int64_t staying_grid(int64_t M, int blocks) {
   const int64_t need = (M + S::R - 1) / S::R, cap = (int64_t)sm100_host::sm_count() * blocks;
@@ -480,18 +525,36 @@ cudaError_t launch_quant(const void* x, const void* residual, int64_t M, int64_t
                flow.stages * row_bytes, stream, x, residual, M, (int)K, gain, h, codes, scales);
 }
 
+// B blocks of an SM as one (1: as they are)
+template <typename S, int B, bool BF16, bool GT16>
+cudaError_t launch_grad_of(const void* h, int64_t M, int64_t K, const float* gain, const void* g_t, const void* g_h,
+                           void* g_x, float* g_gain, float* sums, cudaStream_t stream) {
+  constexpr int row_bytes = S::E * S::kThreads * (2 * (BF16 ? 16 : 32) + (GT16 ? 16 : 32));
+  constexpr Flow flow = flow_for(S::kThreads, row_bytes);
+  using W = Wide<S, B>;
+  static std::atomic<bool> done[sm100_host::kMaxDevices];
+  const int64_t grid = grad_grid(M, flow.blocks / B);
+  cudaError_t e = start(add_rms_grad_kernel<W, BF16, GT16, flow.stages>, done, grid, W::kThreads,
+                        flow.stages * B * row_bytes, stream, h, M, (int)K, gain, g_t, g_h, g_x, g_gain ? sums : nullptr);
+  if (e != cudaSuccess || !g_gain) return e;
+  return sm100_host::launch_pdl(gain_sum_kernel, (unsigned)((K + 31) / 32), kSumWarps * 32, 0, stream, 1, (const float*)sums,
+                                (int)grid, (int)K, g_gain);
+}
+
+// Wide blocks where an SM has at least three rounds of their rows: 8192 bf16
+// rows of 4096 take 47.7 us so and 51.8 as separate blocks, 1001 float rows of
+// 2560 (3.4 rounds) 15.4 and 16.4; but 809 bf16 rows of 5552 (2.7 rounds) 13.5
+// and 11.9, and 64 of 4096 6.8 and 4.9.
+constexpr int kWideRounds = 3;
 template <typename S, bool BF16, bool GT16>
 cudaError_t launch_grad(const void* h, int64_t M, int64_t K, const float* gain, const void* g_t, const void* g_h,
                         void* g_x, float* g_gain, float* sums, cudaStream_t stream) {
-  constexpr int row_bytes = S::E * S::kThreads * (2 * (BF16 ? 16 : 32) + (GT16 ? 16 : 32));
-  constexpr Flow flow = flow_for(S::kThreads, row_bytes);
-  static std::atomic<bool> done[sm100_host::kMaxDevices];
-  const int64_t grid = staying_grid<S>(M, flow.blocks);
-  cudaError_t e = start(add_rms_grad_kernel<S, BF16, GT16, flow.stages, flow.blocks>, done, grid, S::kThreads,
-                        flow.stages * row_bytes, stream, h, M, (int)K, gain, g_t, g_h, g_x, g_gain ? sums : nullptr);
-  if (e != cudaSuccess || !g_gain) return e;
-  return sm100_host::launch_pdl(gain_sum_kernel, (unsigned)((K + 31) / 32), kSumWarps * 32, 0, stream, 1, (const float*)sums,
-                                (int)(grid * S::R), (int)K, g_gain);
+  constexpr int B = flow_for(S::kThreads, S::E * S::kThreads * (2 * (BF16 ? 16 : 32) + (GT16 ? 16 : 32))).blocks;
+  if constexpr (B > 1) {
+    if (M >= (int64_t)kWideRounds * sm100_host::sm_count() * Wide<S, B>::R)
+      return launch_grad_of<S, B, BF16, GT16>(h, M, K, gain, g_t, g_h, g_x, g_gain, sums, stream);
+  }
+  return launch_grad_of<S, 1, BF16, GT16>(h, M, K, gain, g_t, g_h, g_x, g_gain, sums, stream);
 }
 
 }  // namespace
@@ -510,8 +573,7 @@ cudaError_t launch_add_rms_quant(const void* x, const void* residual, bool bf16,
 size_t add_rms_backward_workspace(int64_t M, int64_t K) {
   size_t bytes = 0;
   by_length(K, [&](auto rows) {
-    using S = decltype(rows);
-    bytes = (size_t)staying_grid<S>(M, most_blocks(S::kThreads)) * S::R * (size_t)K * 4;
+    bytes = (size_t)grad_grid(M, most_blocks(decltype(rows)::kThreads)) * (size_t)K * 4;
     return cudaSuccess;
   });
   return bytes;

@@ -608,6 +608,52 @@ def test_add_rms_backward(H, M, K, bf16, gt_bf16):
             assert np.all(np.abs(_np(g_gain) - wg) <= (K / 256 + M / 128 + 350) * 2.0 ** -24 * n)
 
 
+MANY = [(9600, 48), (7300, 1040), (3600, 1536), (2500, 4080), (1300, 8176), (500, 16368)]
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("M,K", MANY)
+def test_add_rms_quant_of_many_rows(H, M, K, bf16, bits):
+    """Batches long enough for the grid that stays: the bits of the same rows in short batches; in place too."""
+    import torch
+    rng = np.random.default_rng(M)
+    x, r = (_as(_values(rng.standard_normal((M, K)), bf16), bf16) for _ in range(2))
+    gain = _dev((1.0 + 0.2 * rng.standard_normal(K)).astype(np.float32))
+    h, q, s = H.hbl_add_rms_quant(x, bits, residual=r, gain=gain)
+    for i in list(range(0, M, max(1, M // 7))) + [M - 30]:
+        j = min(i + 30, M)
+        h1, q1, s1 = H.hbl_add_rms_quant(x[i:j], bits, residual=r[i:j], gain=gain)
+        assert torch.equal(h[i:j], h1) and torch.equal(q[i:j], q1) and torch.equal(s[i:j], s1)
+    h2, q2, s2 = H.hbl_add_rms_quant(x, bits, residual=r, gain=gain, h=r)
+    assert h2 is r and torch.equal(h2, h) and torch.equal(q2, q) and torch.equal(s2, s)
+
+
+@pytest.mark.parametrize("bf16,gt_bf16", [(True, True), (False, False), (True, False), (False, True)])
+@pytest.mark.parametrize("M,K", MANY)
+def test_add_rms_backward_of_many_rows(H, M, K, bf16, gt_bf16):
+    """The wide blocks: a row's gradient has the bits that it has in a short batch, whatever block it falls to, in place
+    too; the gain's is the sum over all rows."""
+    import torch
+    rng = np.random.default_rng(M + 1)
+    h, g_h = (_as(_values(rng.standard_normal((M, K)), bf16), bf16) for _ in range(2))
+    g_t = _as(_values(rng.standard_normal((M, K)), gt_bf16), gt_bf16)
+    gain = _dev((1.0 + 0.2 * rng.standard_normal(K)).astype(np.float32))
+    ws, check = _guarded((H.hbl_add_rms_quant_backward_workspace_bytes(M, K),), torch.uint8)
+    g_x, g_gain = H.hbl_add_rms_quant_backward(h, g_t, gain=gain, g_h=g_h, workspace=ws)
+    check("workspace")
+    for i in list(range(0, M, max(1, M // 7))) + [M - 30]:
+        j = min(i + 30, M)
+        assert torch.equal(g_x[i:j], H.hbl_add_rms_quant_backward(h[i:j], g_t[i:j], gain=gain, g_h=g_h[i:j])[0])
+    n = h.double() / torch.sqrt(h.double().square().mean(1, keepdim=True) + 1e-5)
+    terms = n * g_t.double()
+    # M terms in partial sums of at most M / 128 + 300 terms, each with the error of its n
+    off = (g_gain.double() - terms.sum(0)).abs()
+    assert bool((off <= (K / 256 + M / 128 + 350) * 2.0 ** -24 * terms.abs().sum(0)).all())
+    got, _ = H.hbl_add_rms_quant_backward(h, g_t, gain=gain, g_h=g_h, g_x=g_h)
+    assert got is g_h and torch.equal(got, g_x)
+
+
 def test_add_rms_backward_in_place_and_alone(H):
     """g_x over g_h; without a gain no gain gradient; a gain gradient without a gain is the sum all the same."""
     import torch
