@@ -9,14 +9,16 @@
 // batch, so the first of them (the leader: its predecessor's slot is not the
 // one before, or its own starts a block) finds the run by reading slots alone.
 //
-// A CTA takes a group of rows, one head, and K or V, and works on the runs
+// A CTA takes a group of rows, some heads, and K or V, and works on the runs
 // that begin in its group: long runs with all its threads, short ones (a
 // decode step's single rows) a warp each, the rows held in registers between
-// the maximum and the codes.  Bytes are all there is to it: 2 (4) in and 1 out
-// per value; for few rows, the launch and four dependent reads.  Measured: six
-// prompts of up to 2731 rows (32 heads of 128, 350 MB in and out) 70 us, 5.0
-// TB/s, 76% of a plain copy's rate (eleven instructions a value keep the issue
-// slots 61% busy beside it); 64 single rows 4 us each call in a graph.
+// the maximum and the codes.  The rows of the next head are on their way into
+// shared memory while one is worked on (directly into registers, with more
+// CTAs an SM to hide it, six prompts took 70 us instead of 64).  Bytes are all
+// there is to it: 2 (4) in and 1 out per value; for few rows, the launch and
+// four dependent reads.  Measured: six prompts of up to 2731 rows (32 heads of
+// 128, 350 MB in and out) 64 us, 5.5 TB/s, 84% of a plain copy's rate; 64
+// single rows 4 us each call in a graph.
 #include <cstdint>
 
 #include "common.cuh"
@@ -41,20 +43,18 @@ __device__ __forceinline__ uint32_t code_of(float x, float r, float half, int L)
   return (uint32_t)min(max(c, 0), L);
 }
 
-// A code in the low byte.  With |x| <= gamma the sum lies in [0, L] (a
+// Two codes in the low bytes.  With |x| <= gamma the sum lies in [0, L] (a
 // rounding of r moves it by less than a half), so adding 1.5 * 2^23 rounds it
 // to the nearest integer, ties to even, into the low mantissa bits, and no clip
-// is left to do; a mask keeps what NaN gives within the codes.  Scalar
-// operations: the packed f32x2 multiply and add come out fused, one rounding
-// short of the rule.
-__device__ __forceinline__ uint32_t code_bits(float x, float r, float half) {
-  return __float_as_uint(__fadd_rn(__fadd_rn(__fmul_rn(x, r), half), q::kMagic));
-}
-
-__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a & 0x7FFF7FFFu), "r"(b & 0x7FFF7FFFu));
-  return d;
+// is left to do; a mask keeps what NaN gives within the codes.  The products
+// are scalar: a packed f32x2 multiply comes out fused with the packed addition
+// behind it, one rounding short of the rule.
+__device__ __forceinline__ void code_bits2(float x0, float x1, float r, float half, uint32_t& c0, uint32_t& c1) {
+  asm("{\n\t.reg .b64 P, H, M;\n\t"
+      "mov.b64 P, {%2, %3};\n\tmov.b64 H, {%4, %4};\n\tmov.b64 M, {%5, %5};\n\t"
+      "add.rn.f32x2 P, P, H;\n\tadd.rn.f32x2 P, P, M;\n\tmov.b64 {%0, %1}, P;\n\t}"
+      : "=r"(c0), "=r"(c1)
+      : "f"(__fmul_rn(x0, r)), "f"(__fmul_rn(x1, r)), "f"(half), "f"(q::kMagic));
 }
 
 // eight values of a row, as they lie in memory
@@ -75,25 +75,32 @@ struct Vec8 {
       for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(w[e]);
     }
   }
-  __device__ __forceinline__ float top() const {
+  // the largest magnitudes so far (a NaN gives way to a number): in pairs for bf16, their signs of no meaning
+  __device__ __forceinline__ void join(uint32_t& most) const {
     if constexpr (BF16) {
-      // the larger magnitude of each pair, in pairs (a NaN gives way to a number)
-      const uint32_t m = max_abs2(max_abs2(raw[0].x, raw[0].y), max_abs2(raw[0].z, raw[0].w));
-      return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+      const uint32_t w[4] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) asm("max.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(most) : "r"(w[e]));
     } else {
-      float v[8], m = 0.0f;
+      float v[8], m = __uint_as_float(most);
       values(v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[e]));
-      return m;
+      most = __float_as_uint(m);
     }
+  }
+  static __device__ __forceinline__ float top(uint32_t most) {
+    if constexpr (BF16)
+      return fmaxf(__uint_as_float(most << 16 & 0x7FFFFFFFu), __uint_as_float(most & 0x7FFF0000u));
+    else
+      return __uint_as_float(most);
   }
   __device__ __forceinline__ uint2 codes(float r, float half, uint32_t mask) const {
     float v[8];
     values(v);
     uint32_t q[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) q[e] = code_bits(v[e], r, half);
+    for (int e = 0; e < 8; e += 2) code_bits2(v[e], v[e + 1], r, half, q[e], q[e + 1]);
     return make_uint2(q::gather_low_bytes(q[0], q[1], q[2], q[3]) & mask, q::gather_low_bytes(q[4], q[5], q[6], q[7]) & mask);
   }
 };
@@ -104,63 +111,73 @@ struct Run {
   int slot;
 };
 
-// One run with `threads` threads (a warp or the CTA); reduce: their common
-// maximum, ready before any of them goes on to write.
-template <bool BF16, int kThreadsOf, typename Reduce>
-__device__ __forceinline__ void write_run(const KvAppendArgs& a, const void* x, int64_t stride, int64_t row, int n,
-                                          int slot, int h, uint8_t* all_codes, float* all_scales, int thread,
-                                          Reduce&& reduce) {
-  const int shift = 31 - __clz(a.D / 8);                     // vectors per row and head
+// Where a thread's vectors of a run lie: it keeps its column and goes down the
+// rows (there are at most 32 vectors in one).
+template <bool BF16, int kThreadsOf>
+struct Column {
+  const char* from;
+  int64_t down;
+  int count;  // vectors of the run
+  __device__ __forceinline__ Column(const KvAppendArgs& a, const void* x, int64_t stride, int64_t row, int n, int h, int thread) {
+    constexpr int kSize = BF16 ? 2 : 4;
+    const int shift = 31 - __clz(a.D / 8);  // vectors per row and head
+    from = reinterpret_cast<const char*>(x) +
+           ((row + (thread >> shift)) * stride + (int64_t)h * a.D + ((thread & ((1 << shift) - 1)) << 3)) * kSize;
+    down = (kThreadsOf >> shift) * stride * kSize;
+    count = n << shift;
+  }
+  // a block's worth: no bounds to look at
+  __device__ __forceinline__ bool full() const { return count == kHold<BF16> * kThreadsOf; }
+};
+
+// One run with kThreadsOf threads (a warp or the CTA).  take: the first vectors
+// of the thread; reduce: the threads' common maximum, ready before any of them
+// goes on to write.
+template <bool BF16, int kThreadsOf, typename Take, typename Reduce>
+__device__ __forceinline__ void write_run(const KvAppendArgs& a, const Column<BF16, kThreadsOf>& at, int slot, int h,
+                                          uint8_t* all_codes, float* all_scales, int thread, Take&& take, Reduce&& reduce) {
   const int block_shift = 31 - __clz(a.block);
   const int place = slot & (a.block - 1);
   const int64_t tile = (int64_t)(slot >> block_shift) * a.H + h;
   uint8_t* codes = all_codes + (tile << block_shift) * a.D;
   float* scale = all_scales + tile;
-  const int count = n << shift;
-  // a thread keeps its column and goes down the rows (there are at most 32 vectors in one)
-  constexpr int kSize = BF16 ? 2 : 4;
-  const char* from = reinterpret_cast<const char*>(x) +
-                     ((row + (thread >> shift)) * stride + (int64_t)h * a.D + ((thread & ((1 << shift) - 1)) << 3)) * kSize;
-  const int64_t down = (kThreadsOf >> shift) * stride * kSize;
   const float old = place ? *scale : 0.0f;
   Vec8<BF16> held[kHold<BF16>];
-  float m = 0.0f;
-  const bool full = count == kHold<BF16> * kThreadsOf;  // a block's worth: no bounds to look at
-  if (full) {
+  uint32_t most = 0;
+  const bool full = at.full();
+  const int count = at.count;
+  take(held);
 #pragma unroll
-    for (int j = 0; j < kHold<BF16>; ++j) held[j].load(from + j * down);
-  } else {
-#pragma unroll
-    for (int j = 0; j < kHold<BF16>; ++j) {
-      held[j] = Vec8<BF16>();
-      if (thread + j * kThreadsOf < count) held[j].load(from + j * down);
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < kHold<BF16>; ++j) m = fmaxf(m, held[j].top());
+  for (int j = 0; j < kHold<BF16>; ++j) held[j].join(most);
   // the largest blocks of the widest heads are read twice
   for (int j = kHold<BF16>; thread + j * kThreadsOf < count; ++j) {
     Vec8<BF16> v;
-    v.load(from + j * down);
-    m = fmaxf(m, v.top());
+    v.load(at.from + j * at.down);
+    v.join(most);
   }
-  m = reduce(m);
+  const float m = reduce(Vec8<BF16>::top(most));
   const int L = (1 << a.bits) - 1;
   const uint32_t mask = (uint32_t)L * 0x01010101u;
   const float gamma = fmaxf(old, m);
   const float r = __fdiv_rn((float)L, __fmul_rn(2.0f, __fadd_rn(gamma, 1e-5f))), half = 0.5f * (float)L;
   if (place && gamma > old) {
     const float u = __fdiv_rn(old, (float)L);
-    uint32_t* words = reinterpret_cast<uint32_t*>(codes);
-    for (int i = thread; i < place * a.D / 4; i += kThreadsOf) {
-      const uint32_t w = words[i];
-      uint32_t out = 0;
+    uint4* earlier = reinterpret_cast<uint4*>(codes);
+#pragma unroll 2
+    for (int i = thread; i < place * a.D / 16; i += kThreadsOf) {
+      const uint4 v = earlier[i];
+      const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+      uint32_t out[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int q = (int)((w >> (8 * e)) & 0xFFu);
-        out |= code_of(__fmul_rn((float)(2 * q - L), u), r, half, L) << (8 * e);
+      for (int w = 0; w < 4; ++w) {
+        out[w] = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int q = (int)((words[w] >> (8 * e)) & 0xFFu);
+          out[w] |= code_of(__fmul_rn((float)(2 * q - L), u), r, half, L) << (8 * e);
+        }
       }
-      words[i] = out;
+      earlier[i] = make_uint4(out[0], out[1], out[2], out[3]);
     }
   }
   uint2* to = reinterpret_cast<uint2*>(codes + place * a.D) + thread;
@@ -174,14 +191,26 @@ __device__ __forceinline__ void write_run(const KvAppendArgs& a, const void* x, 
   }
   for (int j = kHold<BF16>; thread + j * kThreadsOf < count; ++j) {
     Vec8<BF16> v;
-    v.load(from + j * down);
+    v.load(at.from + j * at.down);
     to[j * kThreadsOf] = v.codes(r, half, mask);
   }
   if (thread == 0 && !(place && gamma == old)) *scale = gamma;
 }
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads, BF16 ? 6 : 5) kv_append_kernel(const KvAppendArgs a, const int group, const int span) {
+__global__ void __launch_bounds__(kThreads, 5) kv_append_kernel(const KvAppendArgs a, const int group, const int span) {
+  constexpr int kPieces = BF16 ? 1 : 2;                             // 16-byte pieces of a vector
+  constexpr int kStage = kHold<BF16> * kPieces * 16 * kThreads;     // bytes
+  __shared__ __align__(16) uint8_t ring[2 * kStage];
   __shared__ Run runs[2][kMaxGroup];  // long ones, short ones
   __shared__ int count[2];
   __shared__ float tops[2][kWarps];
@@ -228,25 +257,69 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 6 : 5) kv_append_kernel(const
   for (int h = h0; h < h1; ++h) {
     for (int i = warp; i < count[1]; i += kWarps) {
       const Run r = runs[1][i];
-      write_run<BF16, 32>(a, x, stride, row0 + r.row, r.n, r.slot, h, codes, scales, lane, [&](float m) {
+      const Column<BF16, 32> at(a, x, stride, row0 + r.row, r.n, h, lane);
+      auto take = [&](Vec8<BF16> (&held)[kHold<BF16>]) {
+#pragma unroll
+        for (int j = 0; j < kHold<BF16>; ++j) {
+          held[j] = Vec8<BF16>();
+          if (lane + j * 32 < at.count) held[j].load(at.from + j * at.down);
+        }
+      };
+      write_run<BF16, 32>(a, at, r.slot, h, codes, scales, lane, take, [&](float m) {
         return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
       });
     }
   }
-  int parity = 0;
-  for (int i = 0; i < count[0]; ++i) {
-    const Run r = runs[0][i];
-    for (int h = h0; h < h1; ++h) {
-      write_run<BF16, kThreads>(a, x, stride, row0 + r.row, r.n, r.slot, h, codes, scales, tid, [&](float m) {
-        m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
-        if (lane == 0) tops[parity][warp] = m;
-        __syncthreads();
+  // Long runs: the next run's (or head's) vectors are on their way while one is worked on.  A thread copies what it
+  // will read itself, so its own wait is all the ordering there is.
+  int parity = 0, run = 0, h = h0;
+  const int runs_here = count[0];
+  const uint32_t mine = sm100::smem_u32(ring) + tid * 16;
+  auto fetch = [&](int i, int head_of, int stage) {
+    if (i < runs_here) {
+      const Run r = runs[0][i];
+      const Column<BF16, kThreads> at(a, x, stride, row0 + r.row, r.n, head_of, tid);
+      const uint32_t to = mine + stage * kStage;
+      const bool full = at.full();
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, tops[parity][w]);
-        parity ^= 1;
-        return m;
-      });
+      for (int j = 0; j < kHold<BF16>; ++j) {
+        if (full || tid + j * kThreads < at.count) {
+#pragma unroll
+          for (int y = 0; y < kPieces; ++y) cp_async16(to + (j * kPieces + y) * (16 * kThreads), at.from + j * at.down + 16 * y);
+        }
+      }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  fetch(0, h0, 0);
+  while (run < runs_here) {
+    const int next_h = h + 1 < h1 ? h + 1 : h0, next_run = h + 1 < h1 ? run : run + 1;
+    fetch(next_run, next_h, parity ^ 1);
+    const Run r = runs[0][run];
+    const Column<BF16, kThreads> at(a, x, stride, row0 + r.row, r.n, h, tid);
+    auto take = [&](Vec8<BF16> (&held)[kHold<BF16>]) {
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      const bool full = at.full();
+#pragma unroll
+      for (int j = 0; j < kHold<BF16>; ++j) {
+        held[j] = Vec8<BF16>();
+        if (full || tid + j * kThreads < at.count) {
+#pragma unroll
+          for (int y = 0; y < kPieces; ++y) held[j].raw[y] = lds128(mine + parity * kStage + (j * kPieces + y) * (16 * kThreads));
+        }
+      }
+    };
+    write_run<BF16, kThreads>(a, at, r.slot, h, codes, scales, tid, take, [&](float m) {
+      m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+      if (lane == 0) tops[parity][warp] = m;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, tops[parity][w]);
+      parity ^= 1;
+      return m;
+    });
+    run = next_run;
+    h = next_h;
   }
 }
 
@@ -255,7 +328,8 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 6 : 5) kv_append_kernel(const
 cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t stream) {
   // Rows per CTA, then heads: as many as leave about thirty CTAs per SM, so
   // that a decode batch has one row and head a CTA, and a prompt shares the
-  // search for its runs among several heads.
+  // search for its runs among several heads.  (About twelve: 69 us instead of
+  // 64 for the six prompts, the last ones running alone.)
   const int64_t ctas = a.T * a.H * 2, want = (int64_t)sm100_host::sm_count() * 32;
   int group = 1, span = 1;
   while (group < kMaxGroup && ctas / (group * 2) >= want) group *= 2;
