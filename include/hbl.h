@@ -451,7 +451,8 @@ size_t hbl_add_rms_quant_backward_workspace_bytes(int64_t M, int64_t K);
  *   g_x    device, [M][K] of dtype xt (output; may be g_h itself)
  *   g_gain device, K floats (output), or NULL where it is not wanted
  * Sums over a row are float, those over the rows float in fixed order.
- * workspace device, 256-byte aligned. */
+ * workspace device, 256-byte aligned, >= the query's bytes; scratch, of one
+ * call at a time. */
 hbl_status hbl_add_rms_quant_backward(const void* h, hbl_dtype xt, int64_t M, int64_t K, const float* gain,
                                       const void* g_t, hbl_dtype gt, const void* g_h, void* g_x, float* g_gain,
                                       void* workspace, size_t workspace_bytes, cudaStream_t stream);

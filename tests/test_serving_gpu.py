@@ -182,6 +182,30 @@ def test_append_passes_over_rows_without_a_place(H):
         assert np.array_equal(to_host(g[0]), want[0]) and np.array_equal(to_host(g[1]), want[1])
 
 
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("new", [[1, 1], [90, 64]])
+def test_append_of_nan(H, new, bf16):
+    """A NaN takes no part in its block's gamma, its code is one of the levels, and all other codes are as with 0 in its
+    place; the other heads and blocks know nothing of it."""
+    rng = np.random.default_rng(sum(new))
+    heads, D, block, bits = 3, 128, 32, 3
+    slots, _, n = _slots(rng, [10, 0], new, block)
+    x = _values(rng.standard_normal((len(slots), heads, D)), bf16)
+    x[0, 1, 5], x[-1, 2, 127] = 0.0, 0.0
+    kc, ks = _cache(rng, n, heads, block, D, bits)
+    want = ref.append(x, slots, kc, ks, bits)
+    x[0, 1, 5], x[-1, 2, 127] = np.nan, -np.nan
+    state = [_dev(a) for a in (kc, ks, kc, ks)]
+    H.hbl_kv_append(_as(x, bf16), _as(x, bf16), _i32(slots), *state, bits)
+    for codes, scales in (state[:2], state[2:]):
+        codes, same = to_host(codes), want[0].copy()
+        for row, h, d in ((0, 1, 5), (-1, 2, 127)):
+            at = slots[row] // block, h, slots[row] % block, d
+            assert codes[at] < 2 ** bits
+            same[at] = codes[at]
+        assert np.array_equal(codes, same) and np.array_equal(to_host(scales), want[1])
+
+
 def test_append_many_rows(H):
     """A prompt batch long enough that every CTA works: sampled pages against the plain form."""
     rng = np.random.default_rng(12)
