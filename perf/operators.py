@@ -272,7 +272,9 @@ def _plain_append_one(x, slots, codes, scales, bits):
     gamma = torch.where(touched, torch.maximum(old, top), scales)
     grown = (touched & (before > 0)[:, None] & (gamma > scales)).nonzero()
     held = codes[grown[:, 0], grown[:, 1]].float()
-    value = (2.0 * held - L) * (scales[grown[:, 0], grown[:, 1]] / L)[:, None, None]
+    # gamma / L rounded once: torch divides a CUDA tensor by a number as a product with the rounded reciprocal
+    gone = scales[grown[:, 0], grown[:, 1]]
+    value = (2.0 * held - L) * (gone / torch.full_like(gone, L))[:, None, None]
     again = _code(value, gamma[grown[:, 0], grown[:, 1]][:, None, None], bits).to(torch.uint8)
     early = (torch.arange(block, device="cuda")[None] < before[grown[:, 0]][:, None])[:, :, None]
     codes[grown[:, 0], grown[:, 1]] = torch.where(early, again, codes[grown[:, 0], grown[:, 1]])
