@@ -221,6 +221,45 @@ def test_append_many_rows(H):
     assert np.array_equal(to_host(state[2]), want[0]) and np.array_equal(to_host(state[3]), want[1])
 
 
+def _grown_blocks(seed, bits, bf16):
+    """One row into each of thousands of blocks that hold earlier tokens under smaller scales, and the plain form."""
+    rng = np.random.default_rng(seed)
+    n, heads, block, D = 5000, 8, 16, 32
+    codes, _ = _cache(rng, n, heads, block, D, bits)
+    scales = np.exp(rng.uniform(-3, 1, (n, heads))).astype(np.float32)
+    slots = rng.permutation(n) * block + rng.integers(1, block, n)
+    x = _values(rng.standard_normal((n, heads, D)) * 4.0, bf16)
+    want = ref.append(x, slots, codes, scales, bits)
+    assert (want[1] > scales).mean() > 0.95
+    return x, slots, codes, scales, want
+
+
+@pytest.mark.parametrize("bits,bf16", [(8, True), (8, False), (3, True)])
+def test_append_into_thousands_of_growing_blocks(H, bits, bf16):
+    """Enough requantized codes that one reading of gamma / L beside the rule's (a product with the rounded reciprocal)
+    would show: bit for bit the plain form."""
+    x, slots, codes, scales, want = _grown_blocks(40 + bits, bits, bf16)
+    state = [_dev(a) for a in (codes, scales, codes, scales)]
+    H.hbl_kv_append(_as(x, bf16), _as(x, bf16), _i32(slots), *state, bits)
+    for g, w in zip(state, want + want):
+        assert np.array_equal(to_host(g), w)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+def test_the_workloads_plain_write_follows_the_rule(bits):
+    """The plain form that the measured write is compared with, on the same blocks."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "perf", "operators.py")
+    spec = importlib.util.spec_from_file_location("operators", path)
+    ops = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ops)
+    x, slots, codes, scales, want = _grown_blocks(50 + bits, bits, True)
+    dc, ds = _dev(codes), _dev(scales)
+    ops._plain_append_one(_as(x, True), _i32(slots), dc, ds, bits)
+    assert np.array_equal(to_host(dc), want[0]) and np.array_equal(to_host(ds), want[1])
+
+
 # ------------------------------------------------------------------ attention
 
 def _attend(H, rng, new, total, Hq, Hkv, D, block, bits, bf16, o_bf16=None, pad=0, first=0, scale=None, mend=None,
