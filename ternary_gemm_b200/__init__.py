@@ -4,8 +4,11 @@ The functions below carry the names of the C entry points in include/hbl.h and
 only marshal arguments: torch tensors supply device memory and the current
 CUDA stream, every step of the computation runs in libhbl.so.  Outputs that
 the caller does not pass are allocated here with torch (the library itself
-never allocates).  If libhbl.so is missing or fails to load, every call raises
--- there is no CPU fallback.
+never allocates).  With `stream=` a call runs on that stream and its own
+allocations belong to it; tensors that are passed in must be ready there, and
+be kept (or marked, Tensor.record_stream) until the stream is done with them.
+If libhbl.so is missing or fails to load, every call raises -- there is no CPU
+fallback.
 """
 from __future__ import annotations
 
@@ -172,6 +175,22 @@ def _ptr(t) -> ctypes.c_void_p:
     return ctypes.c_void_p(t.data_ptr())
 
 
+def _new(stream, shape, dtype, like, zero=False, scratch=False):
+    """A buffer that the caller did not pass, on the device of `like`, made (and filled) on the stream of the call, so
+    that neither the fill nor a later owner of its memory can come between.  A result (not scratch, which is dropped on
+    return) is marked as used on the caller's current stream too."""
+    torch = _torch()
+    make = torch.zeros if zero else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=like.device)
+    here = torch.cuda.current_stream(like.device)
+    with torch.cuda.stream(stream):
+        t = make(shape, dtype=dtype, device=like.device)
+    if not scratch:
+        t.record_stream(here)
+    return t
+
+
 def _need_cuda(*ts):
     for t in ts:
         if not t.is_cuda or not t.is_contiguous():
@@ -204,11 +223,11 @@ def hbl_pack_ternary(W, packed=None, alpha=None, workspace=None, stream=None):
     _need_cuda(W)
     N, K = W.shape
     if packed is None:
-        packed = torch.empty((N, K // 4), dtype=torch.uint8, device=W.device)
+        packed = _new(stream, (N, K // 4), torch.uint8, W)
     if alpha is None:
-        alpha = torch.empty((1,), dtype=torch.float32, device=W.device)
+        alpha = _new(stream, (1,), torch.float32, W)
     if workspace is None:
-        workspace = torch.empty((max(1, hbl_pack_ternary_workspace_bytes(K, N)),), dtype=torch.uint8, device=W.device)
+        workspace = _new(stream, (max(1, hbl_pack_ternary_workspace_bytes(K, N)),), torch.uint8, W, scratch=True)
     _check(lib().hbl_pack_ternary(_ptr(W), _dtype_code(W), K, N, _ptr(packed), _ptr(alpha), _ptr(workspace),
                                   workspace.numel(), _stream(stream)), "hbl_pack_ternary")
     return packed, alpha
@@ -220,10 +239,9 @@ def hbl_fht_quant(x, bits: int, codes=None, scales=None, stream=None):
     _need_cuda(x)
     M, K = x.shape
     if codes is None:
-        codes = (torch.empty((M, K // 2), dtype=torch.uint8, device=x.device) if bits == 4
-                 else torch.empty((M, K), dtype=torch.int8, device=x.device))
+        codes = _new(stream, (M, K // 2), torch.uint8, x) if bits == 4 else _new(stream, (M, K), torch.int8, x)
     if scales is None:
-        scales = torch.empty((M,), dtype=torch.float32, device=x.device)
+        scales = _new(stream, (M,), torch.float32, x)
     _check(lib().hbl_fht_quant(_ptr(x), _dtype_code(x), M, K, bits, _ptr(codes), _ptr(scales), _stream(stream)),
            "hbl_fht_quant")
     return codes, scales
@@ -235,9 +253,9 @@ def hbl_forward(x, packed, alpha, N: int, bits: int, y=None, y_dtype=None, works
     _need_cuda(x, packed, alpha)
     M, K = x.shape
     if y is None:
-        y = torch.empty((M, N), dtype=y_dtype or x.dtype, device=x.device)
+        y = _new(stream, (M, N), y_dtype or x.dtype, x)
     if workspace is None:
-        workspace = torch.empty((hbl_forward_workspace_bytes(M, K, N, bits),), dtype=torch.uint8, device=x.device)
+        workspace = _new(stream, (hbl_forward_workspace_bytes(M, K, N, bits),), torch.uint8, x, scratch=True)
     _check(lib().hbl_forward(_ptr(x), _dtype_code(x), M, K, _ptr(packed), _ptr(alpha), N, bits, _ptr(y),
                              _dtype_code(y), _ptr(workspace), workspace.numel(), _stream(stream)), "hbl_forward")
     return y
@@ -253,11 +271,11 @@ def hbl_backward(x, packed, alpha, N: int, bits: int, g_y, g_x=None, g_W=None, w
     _need_cuda(x, packed, alpha, g_y)
     M, K = x.shape
     if g_x is None:
-        g_x = torch.empty((M, K), dtype=x.dtype, device=x.device)
+        g_x = _new(stream, (M, K), x.dtype, x)
     if g_W is None:
-        g_W = torch.empty((N, K), dtype=torch.float32, device=x.device)
+        g_W = _new(stream, (N, K), torch.float32, x)
     if workspace is None:
-        workspace = torch.empty((hbl_backward_workspace_bytes(M, K, N, bits),), dtype=torch.uint8, device=x.device)
+        workspace = _new(stream, (hbl_backward_workspace_bytes(M, K, N, bits),), torch.uint8, x, scratch=True)
     _check(lib().hbl_backward(_ptr(x), _dtype_code(x), M, K, _ptr(packed), _ptr(alpha), N, bits, _ptr(g_y),
                               _dtype_code(g_y), _ptr(g_x), _ptr(g_W), _ptr(workspace), workspace.numel(),
                               _stream(stream)), "hbl_backward")
@@ -272,7 +290,7 @@ def hbl_gemm_bf16_f32(A, B, a_mn: bool = False, scale=None, D=None, stream=None)
     Kc, C = B.shape
     R = A.shape[1] if a_mn else A.shape[0]
     if D is None:
-        D = torch.empty((R, C), dtype=torch.float32, device=A.device)
+        D = _new(stream, (R, C), torch.float32, A)
     _check(lib().hbl_gemm_bf16_f32(_ptr(A), 1 if a_mn else 0, _ptr(B), R, C, Kc, _ptr(D),
                                    _ptr(scale) if scale is not None else None, _stream(stream)),
            "hbl_gemm_bf16_f32")
@@ -281,11 +299,10 @@ def hbl_gemm_bf16_f32(A, B, a_mn: bool = False, scale=None, D=None, stream=None)
 
 def hbl_ln_backward(x, g_u, g_x=None, stream=None):
     """LayerNorm backward (no affine): g_x [M][K] of x's dtype from x and float32 g_u."""
-    torch = _torch()
     _need_cuda(x, g_u)
     M, K = x.shape
     if g_x is None:
-        g_x = torch.empty((M, K), dtype=x.dtype, device=x.device)
+        g_x = _new(stream, (M, K), x.dtype, x)
     _check(lib().hbl_ln_backward(_ptr(x), _dtype_code(x), M, K, _ptr(g_u), _ptr(g_x), _stream(stream)),
            "hbl_ln_backward")
     return g_x
@@ -293,11 +310,10 @@ def hbl_ln_backward(x, g_u, g_x=None, stream=None):
 
 def hbl_fht_ln_backward(g, x, g_x=None, stream=None):
     """g_x [M][K] (x's dtype) = LayerNorm backward at x of H g / sqrt(K), g float32 [M][K]."""
-    torch = _torch()
     _need_cuda(g, x)
     M, K = x.shape
     if g_x is None:
-        g_x = torch.empty((M, K), dtype=x.dtype, device=x.device)
+        g_x = _new(stream, (M, K), x.dtype, x)
     _check(lib().hbl_fht_ln_backward(_ptr(g), _ptr(x), _dtype_code(x), M, K, _ptr(g_x), _stream(stream)),
            "hbl_fht_ln_backward")
     return g_x
@@ -309,9 +325,9 @@ def hbl_kv_quant(x, bits: int, codes=None, scales=None, stream=None):
     _need_cuda(x)
     rows, D = x.shape
     if codes is None:
-        codes = torch.empty((rows, D), dtype=torch.uint8, device=x.device)
+        codes = _new(stream, (rows, D), torch.uint8, x)
     if scales is None:
-        scales = torch.empty((rows,), dtype=torch.float32, device=x.device)
+        scales = _new(stream, (rows,), torch.float32, x)
     _check(lib().hbl_kv_quant(_ptr(x), _dtype_code(x), rows, D, bits, _ptr(codes), _ptr(scales), _stream(stream)),
            "hbl_kv_quant")
     return codes, scales
@@ -323,7 +339,7 @@ def hbl_fht(x, t=None, stream=None):
     _need_cuda(x)
     M, K = x.shape
     if t is None:
-        t = torch.empty((M, K), dtype=torch.float32, device=x.device)
+        t = _new(stream, (M, K), torch.float32, x)
     _check(lib().hbl_fht(_ptr(x), _dtype_code(x), M, K, _ptr(t), _stream(stream)), "hbl_fht")
     return t
 
@@ -338,12 +354,11 @@ def hbl_pack_ternary_rotated(W, packed=None, alpha=None, workspace=None, stream=
     _need_cuda(W)
     N, K = W.shape
     if packed is None:
-        packed = torch.empty((N, K // 4), dtype=torch.uint8, device=W.device)
+        packed = _new(stream, (N, K // 4), torch.uint8, W)
     if alpha is None:
-        alpha = torch.empty((1,), dtype=torch.float32, device=W.device)
+        alpha = _new(stream, (1,), torch.float32, W)
     if workspace is None:
-        workspace = torch.empty((hbl_pack_ternary_rotated_workspace_bytes(K, N),), dtype=torch.uint8,
-                                device=W.device)
+        workspace = _new(stream, (hbl_pack_ternary_rotated_workspace_bytes(K, N),), torch.uint8, W, scratch=True)
     _check(lib().hbl_pack_ternary_rotated(_ptr(W), _dtype_code(W), K, N, _ptr(packed), _ptr(alpha),
                                           _ptr(workspace), workspace.numel(), _stream(stream)),
            "hbl_pack_ternary_rotated")
@@ -356,10 +371,9 @@ def hbl_norm_quant(x, bits: int, norm: int = HBL_NORM_LAYER, codes=None, scales=
     _need_cuda(x)
     M, K = x.shape
     if codes is None:
-        codes = (torch.empty((M, K // 2), dtype=torch.uint8, device=x.device) if bits == 4
-                 else torch.empty((M, K), dtype=torch.int8, device=x.device))
+        codes = _new(stream, (M, K // 2), torch.uint8, x) if bits == 4 else _new(stream, (M, K), torch.int8, x)
     if scales is None:
-        scales = torch.empty((M,), dtype=torch.float32, device=x.device)
+        scales = _new(stream, (M,), torch.float32, x)
     _check(lib().hbl_norm_quant(_ptr(x), _dtype_code(x), M, K, int(norm), bits, _ptr(codes), _ptr(scales),
                                 _stream(stream)), "hbl_norm_quant")
     return codes, scales
@@ -370,7 +384,7 @@ def hbl_debug_norm(x, norm: int = HBL_NORM_LAYER, t=None, stream=None):
     _need_cuda(x)
     M, K = x.shape
     if t is None:
-        t = torch.empty((M, K), dtype=torch.float32, device=x.device)
+        t = _new(stream, (M, K), torch.float32, x)
     _check(lib().hbl_debug_norm(_ptr(x), _dtype_code(x), M, K, int(norm), _ptr(t), _stream(stream)),
            "hbl_debug_norm")
     return t
@@ -379,11 +393,10 @@ def hbl_debug_norm(x, norm: int = HBL_NORM_LAYER, t=None, stream=None):
 def hbl_forward_noalloc(x, packed, alpha, N: int, bits: int, y=None, y_dtype=None, stream=None):
     """hbl_forward without a workspace, for callers that cannot allocate device memory: the library's
     fixed 32 MiB area is used instead (shapes needing more are rejected; concurrent calls race on it)."""
-    torch = _torch()
     _need_cuda(x, packed, alpha)
     M, K = x.shape
     if y is None:
-        y = torch.empty((M, N), dtype=y_dtype or x.dtype, device=x.device)
+        y = _new(stream, (M, N), y_dtype or x.dtype, x)
     _check(lib().hbl_forward_noalloc(_ptr(x), _dtype_code(x), M, K, _ptr(packed), _ptr(alpha), N, bits, _ptr(y),
                                      _dtype_code(y), _stream(stream)), "hbl_forward_noalloc")
     return y
@@ -395,9 +408,9 @@ def hbl_fht_quant_i8(x, bits: int, codes=None, scales=None, stream=None):
     _need_cuda(x)
     M, K = x.shape
     if codes is None:
-        codes = torch.empty((M, K), dtype=torch.int8, device=x.device)
+        codes = _new(stream, (M, K), torch.int8, x)
     if scales is None:
-        scales = torch.empty((M,), dtype=torch.float32, device=x.device)
+        scales = _new(stream, (M,), torch.float32, x)
     _check(lib().hbl_fht_quant_i8(_ptr(x), _dtype_code(x), M, K, bits, _ptr(codes), _ptr(scales),
                                   _stream(stream)), "hbl_fht_quant_i8")
     return codes, scales
@@ -409,7 +422,7 @@ def hbl_widen_ternary(packed, K: int, w=None, stream=None):
     _need_cuda(packed)
     N = packed.shape[0]
     if w is None:
-        w = torch.empty((N, K), dtype=torch.int8, device=packed.device)
+        w = _new(stream, (N, K), torch.int8, packed)
     _check(lib().hbl_widen_ternary(_ptr(packed), K, N, _ptr(w), _stream(stream)), "hbl_widen_ternary")
     return w
 
@@ -422,7 +435,7 @@ def hbl_gemm_tern_dequant(codes, packed, scales, alpha, y=None, y_dtype=None, st
     M, K = codes.shape[0], codes.shape[1] * 2
     N = packed.shape[0]
     if y is None:
-        y = torch.empty((M, N), dtype=y_dtype or torch.bfloat16, device=codes.device)
+        y = _new(stream, (M, N), y_dtype or torch.bfloat16, codes)
     _check(lib().hbl_gemm_tern_dequant(_ptr(codes), _ptr(packed), M, N, K, _ptr(scales), _ptr(alpha), _ptr(y),
                                        _dtype_code(y), _stream(stream)), "hbl_gemm_tern_dequant")
     return y
@@ -435,7 +448,7 @@ def hbl_gemm_dequant(A, w, scales, alpha, y=None, y_dtype=None, stream=None):
     M, K = A.shape
     N = w.shape[0]
     if y is None:
-        y = torch.empty((M, N), dtype=y_dtype or torch.bfloat16, device=A.device)
+        y = _new(stream, (M, N), y_dtype or torch.bfloat16, A)
     _check(lib().hbl_gemm_dequant(_ptr(A), _ptr(w), M, N, K, _ptr(scales), _ptr(alpha), _ptr(y), _dtype_code(y),
                                   _stream(stream)), "hbl_gemm_dequant")
     return y
@@ -449,7 +462,7 @@ def hbl_gemv_ternary_dequant(A, packed, scales, alpha, y=None, y_dtype=None, str
     M, K = A.shape
     N = packed.shape[0]
     if y is None:
-        y = torch.empty((M, N), dtype=y_dtype or torch.bfloat16, device=A.device)
+        y = _new(stream, (M, N), y_dtype or torch.bfloat16, A)
     _check(lib().hbl_gemv_ternary_dequant(_ptr(A), _ptr(packed), M, N, K, _ptr(scales), _ptr(alpha), _ptr(y),
                                           _dtype_code(y), _stream(stream)), "hbl_gemv_ternary_dequant")
     return y
@@ -526,7 +539,7 @@ def hbl_kv_plan(cached, added, free_blocks, taken, table, block: int, T: int, to
     torch = _torch()
     dev, i32 = _here(table), torch.int32
     B, width = table.shape
-    new = lambda n: torch.empty((n,), dtype=i32, device=table.device)  # noqa: E731
+    new = lambda n: _new(stream, (n,), i32, table)  # noqa: E731
     total = new(B) if total is None else total
     row_start = new(B + 1) if row_start is None else row_start
     slots = new(T) if slots is None else slots
@@ -580,9 +593,9 @@ def hbl_kv_attention(q, row_start, total, table, k_codes, k_scales, v_codes, v_s
         raise ValueError("q has head dimension %d, the cache %d" % (Dq, D))
     B, width = table.shape
     if o is None:
-        o = torch.zeros((T, Hq, D), dtype=o_dtype or q.dtype, device=q.device)
+        o = _new(stream, (T, Hq, D), o_dtype or q.dtype, q, zero=True)
     if workspace is None:
-        workspace = torch.empty((hbl_kv_attention_workspace_bytes(T, Hq, Hkv, D, B),), dtype=torch.uint8, device=q.device)
+        workspace = _new(stream, (hbl_kv_attention_workspace_bytes(T, Hq, Hkv, D, B),), torch.uint8, q, scratch=True)
     _demand_line(dev, i32, ("row_start", row_start, B + 1), ("total", total, B), ("table", table, B * width))
     _demand_line(dev, workspace.dtype, ("workspace", workspace, workspace.numel()))
     _demand(dev, ("o", o, None, (T, Hq, D)))
@@ -609,11 +622,11 @@ def hbl_add_rms_quant(x, bits: int, residual=None, gain=None, h=None, codes=None
     dev, dtype = _here(x), x.dtype
     M, K = x.shape
     if h is None:
-        h = torch.empty_like(x)
+        h = _new(stream, (M, K), dtype, x)
     if codes is None:
-        codes = torch.empty((M, K), dtype=torch.int8, device=x.device)
+        codes = _new(stream, (M, K), torch.int8, x)
     if scales is None:
-        scales = torch.empty((M,), dtype=torch.float32, device=x.device)
+        scales = _new(stream, (M,), torch.float32, x)
     n = M * K
     _demand_line(dev, dtype, ("x", x, n), ("h", h, n))
     _demand_line(dev, torch.int8, ("codes", codes, n))
@@ -639,11 +652,11 @@ def hbl_add_rms_quant_backward(h, g_t, gain=None, g_h=None, g_x=None, g_gain=Non
     dev, dtype, f32 = _here(h), h.dtype, torch.float32
     M, K = h.shape
     if g_x is None:
-        g_x = torch.empty_like(h)
+        g_x = _new(stream, (M, K), dtype, h)
     if g_gain is None and gain is not None:
-        g_gain = torch.empty((K,), dtype=f32, device=h.device)
+        g_gain = _new(stream, (K,), f32, h)
     if workspace is None:
-        workspace = torch.empty((hbl_add_rms_quant_backward_workspace_bytes(M, K),), dtype=torch.uint8, device=h.device)
+        workspace = _new(stream, (hbl_add_rms_quant_backward_workspace_bytes(M, K),), torch.uint8, h, scratch=True)
     n = M * K
     _demand_line(dev, dtype, ("h", h, n), ("g_x", g_x, n))
     _demand_line(dev, g_t.dtype, ("g_t", g_t, n))
@@ -665,7 +678,7 @@ def hbl_debug_ln_fht(x, t=None, stream=None):
     _need_cuda(x)
     M, K = x.shape
     if t is None:
-        t = torch.empty((M, K), dtype=torch.float32, device=x.device)
+        t = _new(stream, (M, K), torch.float32, x)
     _check(lib().hbl_debug_ln_fht(_ptr(x), _dtype_code(x), M, K, _ptr(t), _stream(stream)), "hbl_debug_ln_fht")
     return t
 
@@ -675,10 +688,9 @@ def hbl_quant_from_f32(t, bits: int, codes=None, scales=None, stream=None):
     _need_cuda(t)
     M, K = t.shape
     if codes is None:
-        codes = (torch.empty((M, K // 2), dtype=torch.uint8, device=t.device) if bits == 4
-                 else torch.empty((M, K), dtype=torch.int8, device=t.device))
+        codes = _new(stream, (M, K // 2), torch.uint8, t) if bits == 4 else _new(stream, (M, K), torch.int8, t)
     if scales is None:
-        scales = torch.empty((M,), dtype=torch.float32, device=t.device)
+        scales = _new(stream, (M,), torch.float32, t)
     _check(lib().hbl_quant_from_f32(_ptr(t), M, K, bits, _ptr(codes), _ptr(scales), _stream(stream)),
            "hbl_quant_from_f32")
     return codes, scales
@@ -690,7 +702,7 @@ def hbl_gemm_i8_i32(A, B, acc=None, stream=None):
     M, K = A.shape
     N = B.shape[0]
     if acc is None:
-        acc = torch.empty((M, N), dtype=torch.int32, device=A.device)
+        acc = _new(stream, (M, N), torch.int32, A)
     _check(lib().hbl_gemm_i8_i32(_ptr(A), _ptr(B), M, N, K, _ptr(acc), _stream(stream)), "hbl_gemm_i8_i32")
     return acc
 

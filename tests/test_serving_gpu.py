@@ -895,6 +895,58 @@ def test_two_streams_at_once(H):
         assert torch.equal(again[0], gx[j][0]) and torch.equal(again[1], gx[j][1])
 
 
+def _busy(stream, cycles=40_000_000):
+    """Some 20 ms of nothing on a stream."""
+    import torch
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(cycles)
+
+
+def test_results_on_a_stream_that_is_not_the_current_one(H):
+    """stream= with buffers that the call makes itself: what it fills and what it computes is in one order, however far
+    behind the current stream is."""
+    import torch
+    rng = np.random.default_rng(61)
+    total, table = rng.integers(1, 300, 6), rng.permutation(60).reshape(6, 10)
+    cache = [_dev(a) for a in _cache(rng, 60, 2, 32, 64, 8) + _cache(rng, 60, 2, 32, 64, 8)]
+    q = _as(rng.standard_normal((9, 8, 64)), True)              # three rows behind the last request
+    args = (q, _i32(range(7)), _i32(total), _i32(table), *cache)
+    want = H.hbl_kv_attention(*args)
+    torch.cuda.synchronize()
+    other = torch.cuda.Stream()
+    _busy(torch.cuda.current_stream())
+    got = H.hbl_kv_attention(*args, stream=other)
+    torch.cuda.synchronize()
+    assert bool((want[:6] != 0).any()) and torch.equal(got, want)
+
+
+def test_memory_of_a_call_on_another_stream_is_its_own(H):
+    """While a call with stream= has yet to run, allocations on the current stream do not get its scratch or a result
+    that was dropped."""
+    import torch
+    rng = np.random.default_rng(62)
+    total, table = rng.integers(1, 300, 6), rng.permutation(60).reshape(6, 10)
+    cache = [_dev(a) for a in _cache(rng, 60, 2, 32, 64, 8) + _cache(rng, 60, 2, 32, 64, 8)]
+    q = _as(rng.standard_normal((6, 8, 64)), True)
+    args = (q, _i32(range(7)), _i32(total), _i32(table), *cache)
+    x, gain = _as(rng.standard_normal((500, 2048)), True), torch.ones(2048, device="cuda")
+    packed, alpha = H.hbl_pack_ternary(_as(rng.standard_normal((1024, 2048)), True))
+    calls = [(lambda s: H.hbl_kv_attention(*args, stream=s), H.hbl_kv_attention_workspace_bytes(6, 8, 2, 64, 6)),
+             (lambda s: H.hbl_add_rms_quant_backward(x, x, gain=gain, stream=s),
+              H.hbl_add_rms_quant_backward_workspace_bytes(500, 2048)),
+             (lambda s: H.hbl_add_rms_quant(x, 8, gain=gain, stream=s), 2 * 500 * 2048),      # h
+             (lambda s: H.hbl_forward(x, packed, alpha, 1024, 8, stream=s), H.hbl_forward_workspace_bytes(500, 2048, 1024, 8))]
+    other = torch.cuda.Stream()
+    for call, size in calls:
+        call(None)
+        torch.cuda.synchronize()
+        _busy(other)
+        call(other)
+        mine = [torch.full((size,), 7, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        torch.cuda.synchronize()
+        assert all(bool((m == 7).all()) for m in mine)
+
+
 def test_the_binding_refuses(H):
     """Wrong types, shapes, strides, devices: nothing is launched on tensors that do not fit."""
     import torch
