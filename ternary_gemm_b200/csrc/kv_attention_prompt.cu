@@ -538,7 +538,10 @@ kv_attention_prompt_kernel(const KvAttentionArgs a, const int splits, int* err) 
       if (!ok) break;
     }
     // ---- o = (2 O + sum of the weights) / l
-    if (ok && mine > 0) ok = await(&ofinal[mt], 0, abort_flag, err);
+    // Below, a warp of 128-value rows writes over the Q rows of its neighbours: they have all been written (and turned)
+    // once qready completes, and read once the tile's products have ended.  A row tile that sees no token has no
+    // products to wait for, so it waits for the Q rows alone.
+    if (ok) ok = mine > 0 ? await(&ofinal[mt], 0, abort_flag, err) : await(qready, 0, abort_flag, err);
     fence_after();
     if (ok && used > 1) {
       // a part: unscaled, under this CTA's reference
@@ -563,7 +566,7 @@ kv_attention_prompt_kernel(const KvAttentionArgs a, const int splits, int* err) 
       if (live) parts.ml[(int64_t)blockIdx.x * kRows + t] = make_float2(ref, l);
     } else if (ok) {
       const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
-      // through the warp's part of the Q tile, whose products have ended, so that lanes write whole rows
+      // through the warp's part of the Q tile, free by now, so that lanes write whole rows
       const uint32_t stage = q_at + mt * S::kTile + (warp & 3) * (32 * D * 2);
       constexpr int kLanes = D / 8;
       auto place = [&](int r, int piece) { return stage + r * (D * 2) + ((piece ^ (r & 7)) << 4); };

@@ -372,6 +372,29 @@ def test_attention_pages_outside_the_cache(H):
         assert np.all(got[lo:lo + new[2]] == 0)
 
 
+@pytest.mark.parametrize("o_bf16", [True, False])
+@pytest.mark.parametrize("D", [64, 128])
+def test_prompt_rows_that_see_no_token(H, D, o_bf16):
+    """Hundreds of rows over no token, or over far fewer than there are rows, beside a whole prompt: whole row tiles see
+    nothing and give exactly 0, in every one of many runs."""
+    import torch
+    rng = np.random.default_rng(63 + D)
+    new, total = [300, 400, 350], np.array([0, 60, 350])
+    got, want = _attend(H, rng, new, total, 8, 2, D, 64, 8, True, o_bf16)
+    assert np.all(want[:640] == 0) and np.all(got[:640] == 0) and np.any(got[640:] != 0)
+    cache = [_dev(a) for a in _cache(rng, 20, 2, 64, D, 8) + _cache(rng, 20, 2, 64, D, 8)]
+    q = _as(rng.standard_normal((1050, 8, D)), True)
+    o = torch.empty((1050, 8, D), dtype=torch.bfloat16 if o_bf16 else torch.float32, device="cuda")
+    ws = torch.empty((H.hbl_kv_attention_workspace_bytes(1050, 8, 2, D, 3),), dtype=torch.uint8, device="cuda")
+    rows, table = _i32([0, 300, 700, 1050]), _i32(np.arange(18).reshape(3, 6))
+    first = None
+    for i in range(60):
+        o.fill_(3.0)
+        H.hbl_kv_attention(q, rows, _i32(total), table, *cache, o=o, workspace=ws)
+        first = o.clone() if first is None else first
+        assert bool((o[:640] == 0).all()) and torch.equal(o, first), i
+
+
 def test_attention_longer_than_its_table(H):
     """A length past the table: the tokens that the table has are seen."""
     rng = np.random.default_rng(7)
