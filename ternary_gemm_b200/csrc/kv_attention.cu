@@ -204,6 +204,8 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+__device__ __forceinline__ Shrink shrink(float d) { return {ex2(fmaxf(d, -100.0f)), ex2(fminf(d + 100.0f, 0.0f))}; }
+
 // 8 x 8 matrix of fp16 pairs across the warp, transposed
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   uint32_t d;
@@ -521,8 +523,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, NT, F32)) kv_attent
         const float k = a.k_scales[tile], v = a.v_scales[tile];
         ku = __fdiv_rn(k, (float)L);
         const float vu = __fdiv_rn(v, (float)L);
-        kind = vu >= 1e-30f ? 0 : 1;
-        lu = __log2f(fmaxf(vu, 1e-30f));
+        kind = vu >= kLeastValueScale ? 0 : 1;
+        lu = kind == 0 ? __log2f(vu) : kLeastValueLog;
       }
     };
     id_now = page_of(0);
@@ -615,14 +617,15 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, NT, F32)) kv_attent
       });
 
       int kind[2];
-      float ku[2], lu[2], inv_vu[2];
+      float ku[2], lu[2], inv_vu[2], lift[2];  // lift: what takes u out of the weights of zeros for the sum
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const int from = (2 * i + half) & 31;
         kind[half] = __shfl_sync(0xffffffffu, kind_now, from);
         ku[half] = __shfl_sync(0xffffffffu, ku_now, from);
         lu[half] = __shfl_sync(0xffffffffu, lu_now, from);
-        inv_vu[half] = ex2(-lu[half]);
+        lift[half] = kind[half] == 1 ? kSumLog - kLeastValueLog : 0.0f;
+        inv_vu[half] = kind[half] == 1 ? 1.0f : ex2(-lu[half]) * kSumScale;
       }
       const int tok0 = (first + 2 * i) * kTok;
       const bool masked = kind[0] == 2 || kind[1] == 2 || tok0 + kStep > all_see;
@@ -657,18 +660,20 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, NT, F32)) kv_attent
               m[nt][x], row_max(fmaxf(fmaxf(p[0][0][x], p[0][1][x]), fmaxf(p[1][0][x], p[1][1][x]))));
           // a row that has seen nothing keeps -inf, with 0 in its place in the differences
           const float base = top == -INFINITY ? 0.0f : top, off = kTop - base;
-          grow[nt][x] = ex2(m[nt][x] - base);
+          const Shrink by = shrink(m[nt][x] - base);
+          grow[nt][x] = by.near;
+          l[nt][x] *= by.far;
           grows |= grow[nt][x] != 1.0f;
           m[nt][x] = top;
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            p[half][0][x] = ex2(p[half][0][x] + off);
-            p[half][1][x] = ex2(p[half][1][x] + off);
+            p[half][0][x] = ex2(p[half][0][x] + (off + lift[half]));
+            p[half][1][x] = ex2(p[half][1][x] + (off + lift[half]));
           }
         }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          // a block whose values are all zero (below 1e-30) takes part in the sum alone
+          // a block whose values are all zero takes part in the sum alone
           const bool zero = kind[half] == 1;
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
@@ -745,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, NT, F32)) kv_attent
         const float sum = row_sum(l[nt][x]), ws = row_sum(w_sum[nt][x]);
         const int in_tile = nt * 8 + 2 * c + x, row = row0 + in_tile;
         if (row >= r.n * g) continue;
-        const float inv = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
+        const float inv = sum == 0.0f ? 0.0f : __fdiv_rn(kSumScale, sum);
         const int64_t at = ((int64_t)(r.row0 + row / g) * a.Hq + (int64_t)h * g + row % g) * D;
 #pragma unroll
         for (int s = 0; s < kSegs; ++s) {
@@ -781,15 +786,16 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, NT, F32)) kv_attent
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) v[i] = 0.0f;
         for (int w = 0; w < shares; ++w) {
-          const float f = ex2(cta_ml[w][y].x - base);
-          sum = fmaf(f, cta_ml[w][y].y, sum);
+          const Shrink by = shrink(cta_ml[w][y].x - base);
+          const float f = by.near;
+          sum = fmaf(f, by.far * cta_ml[w][y].y, sum);
           const float* from = reinterpret_cast<const float*>(smem + w * kStages * kStage) + y * D;
 #pragma unroll
           for (int i = 0; i < D / 32; ++i) v[i] = fmaf(f, from[i * 32 + lane], v[i]);
         }
         const int row = row0 + y;
         const int64_t at = ((int64_t)(r.row0 + row / g) * a.Hq + (int64_t)h * g + row % g) * D;
-        const float inv = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
+        const float inv = sum == 0.0f ? 0.0f : __fdiv_rn(kSumScale, sum);
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
           if (!all)
@@ -888,9 +894,11 @@ __global__ void __launch_bounds__(kJoinThreads) kv_attention_join_kernel(const K
         float now = top;
 #pragma unroll
         for (int e = 0; e < kAhead; ++e) now = fmaxf(now, ml[e].x);
-        const float base = now == -INFINITY ? 0.0f : now, f0 = ex2(top - base);
+        const float base = now == -INFINITY ? 0.0f : now;
+        const Shrink to_now = shrink(top - base);
+        const float f0 = to_now.near;
         top = now;
-        sum *= f0;
+        sum = sum * to_now.far * f0;
 #pragma unroll
         for (int j = 0; j < kCols; ++j)
 #pragma unroll
@@ -898,8 +906,9 @@ __global__ void __launch_bounds__(kJoinThreads) kv_attention_join_kernel(const K
 #pragma unroll
         for (int e = 0; e < kAhead; ++e) {
           if (p0 + e < count) {
-            const float f = ex2(ml[e].x - base);
-            sum = fmaf(f, ml[e].y, sum);
+            const Shrink by = shrink(ml[e].x - base);
+            const float f = by.near;
+            sum = fmaf(f, by.far * ml[e].y, sum);
 #pragma unroll
             for (int j = 0; j < kCols; ++j)
 #pragma unroll
@@ -907,7 +916,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv_attention_join_kernel(const K
           }
         }
       }
-      const float inv = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
+      const float inv = sum == 0.0f ? 0.0f : __fdiv_rn(kSumScale, sum);
       const int row = rec.row + y;
       const int64_t at = ((int64_t)(rec.row0 + row / g) * a.Hq + (int64_t)rec.h * g + row % g) * D + lane * V;
 #pragma unroll

@@ -187,16 +187,20 @@ __device__ __forceinline__ void sts128(uint32_t at, uint32_t a, uint32_t b, uint
 // place of 16 bytes (eight fp16 values) of row t in a block of 64 values
 __device__ __forceinline__ uint32_t swizzled(int t, int piece) { return (uint32_t)(t * 128 + ((piece ^ (t & 7)) << 4)); }
 
+__device__ __forceinline__ Shrink shrink(float d) { return {ex2(fmaxf(d, -100.0f)), ex2(fminf(d + 100.0f, 0.0f))}; }
+
 // What a row's scores of sixteen tokens of one page are to be multiplied by and
-// added to, the inverse of the values' scale, and whether any value is not 0.
+// added to, the inverse of the values' scale as it is in the weights, and what
+// the weights count for the reference: 1, or less for a page whose values are
+// all zero, the weights of which stand as they go into the sum (0: no page).
 struct Page {
-  float f2, c, inv;
-  bool some;
+  float f2, c, inv, part;
+  __device__ __forceinline__ bool some() const { return part == 1.0f; }
 };
 __device__ __forceinline__ Page page_at(uint32_t pages, int grp, float q_scale, float q_sum) {
   const uint4 p = lds128(pages + grp * 16);
   const float f = q_scale * __uint_as_float(p.x);
-  return {2.0f * f, fmaf(q_sum, f, __uint_as_float(p.y)), __uint_as_float(p.z), p.w != 0};
+  return {2.0f * f, fmaf(q_sum, f, __uint_as_float(p.y)), __uint_as_float(p.z), __uint_as_float(p.w)};
 }
 
 // The CTA's item: which request, its rows, and where they stand.
@@ -457,11 +461,11 @@ kv_attention_prompt_kernel(const KvAttentionArgs a, const int splits, int* err) 
 #pragma unroll
             for (int e = 0; e < 8; ++e) w[grp][e] = pack2(v[2 * e], v[2 * e + 1]);
             s0 += s1;
-            most += s0;
+            most = fmaf(s0, p.part, most);
             sum = fmaf(s0, p.inv, sum);
             // a page whose values are all zero takes part in the sum alone
-            all += p.some ? s0 : 0.0f;
-            if (!p.some) {
+            all += p.some() ? s0 : 0.0f;
+            if (!p.some()) {
 #pragma unroll
               for (int e = 0; e < 8; ++e) w[grp][e] = 0u;
             }
@@ -473,12 +477,13 @@ kv_attention_prompt_kernel(const KvAttentionArgs a, const int splits, int* err) 
 #pragma unroll 1
           for (int grp = 0; grp < 4; ++grp) {
             const Page p = page_at(pages, 4 * half + grp, q_scale, q_sum);
+            const float c = p.some() ? p.c : p.c + (kLeastValueLog - kSumLog);
             uint32_t s[16];
             tmem_ld16(from + 16 * grp, s);
             landed(s);
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-              if (first + 16 * grp + e < lim) top = fmaxf(top, fmaf(__uint_as_float(s[e]), p.f2, p.c));
+              if (first + 16 * grp + e < lim) top = fmaxf(top, fmaf(__uint_as_float(s[e]), p.f2, c));
           }
           return top;
         };
@@ -495,7 +500,8 @@ kv_attention_prompt_kernel(const KvAttentionArgs a, const int splits, int* err) 
         if (__any_sync(0xffffffffu, follow)) {
           const float top = maximum();
           const float next = follow ? fmaxf(ref, top) : ref;
-          const float grow = ref == -INFINITY ? 0.0f : ex2(ref - next);
+          const Shrink to_next = shrink(ref == -INFINITY ? -INFINITY : ref - next);
+          const float grow = to_next.near;
           if (i + half > 0) {
             // the products up to the half before this one (the one before that is known to have ended)
             if (!await(&odone[mt], (uint32_t)(half ^ 1), abort_flag, err)) {
@@ -515,7 +521,7 @@ kv_attention_prompt_kernel(const KvAttentionArgs a, const int splits, int* err) 
             }
           }
           if (follow && next != ref) {
-            l *= grow;
+            l = l * to_next.far * grow;
             ws *= grow;
             ref = next;
           }
@@ -565,7 +571,7 @@ kv_attention_prompt_kernel(const KvAttentionArgs a, const int splits, int* err) 
       }
       if (live) parts.ml[(int64_t)blockIdx.x * kRows + t] = make_float2(ref, l);
     } else if (ok) {
-      const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
+      const float inv = l == 0.0f ? 0.0f : __fdiv_rn(kSumScale, l);
       // through the warp's part of the Q tile, free by now, so that lanes write whole rows
       const uint32_t stage = q_at + mt * S::kTile + (warp & 3) * (32 * D * 2);
       constexpr int kLanes = D / 8;
@@ -675,10 +681,11 @@ kv_attention_prompt_kernel(const KvAttentionArgs a, const int splits, int* err) 
       if (lane < 2) {
         const bool there = (lane == 0 ? id[0] : id[1]) >= 0;
         const float vu = __fdiv_rn(vs, (float)L);
-        const bool some = vu >= 1e-30f;
-        const float lu = __log2f(some ? vu : 1e-30f);
+        const bool some = vu >= kLeastValueScale;
+        const float lu = some ? __log2f(vu) : kSumLog;
         meta[(i % kMeta) * 8 + cw * 2 + lane] =
-            there ? make_float4(__fdiv_rn(ks, (float)L), lu, ex2(-lu), some ? 1.0f : 0.0f)
+            there ? make_float4(__fdiv_rn(ks, (float)L), lu, some ? ex2(-lu) * kSumScale : 1.0f,
+                                some ? 1.0f : kLeastValueScale / kSumScale)
                   : make_float4(0.0f, -INFINITY, 0.0f, 0.0f);
       }
       convert(k_at + st * S::kTile, id, kv);
@@ -794,8 +801,9 @@ __global__ void __launch_bounds__(256) kv_attention_prompt_join_kernel(const KvA
     float top = ml.x;
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float f = ex2(ml.x - (top == -INFINITY ? 0.0f : top));
-    float sum = f * ml.y;
+    const Shrink by = shrink(ml.x - (top == -INFINITY ? 0.0f : top));
+    const float f = by.near;
+    float sum = f * (by.far * ml.y);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     float acc[V];
@@ -812,7 +820,7 @@ __global__ void __launch_bounds__(256) kv_attention_prompt_join_kernel(const KvA
         acc[i + 1] = fmaf(by, v.y, acc[i + 1]);
       }
     }
-    const float inv = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
+    const float inv = sum == 0.0f ? 0.0f : __fdiv_rn(kSumScale, sum);
     const int row = it.first + t;
     const int64_t to = ((int64_t)(it.row0 + row / g) * a.Hq + (int64_t)it.h * g + row % g) * D + lane * V;
 #pragma unroll

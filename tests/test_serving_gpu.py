@@ -433,6 +433,36 @@ def test_attention_ignores_what_is_masked(H):
     assert torch.equal(outs[0], outs[1]) and bool(torch.isfinite(outs[0]).all())
 
 
+@pytest.mark.parametrize("bf16", [True, False])
+def test_attention_behind_a_long_run_of_zeros(H, bf16):
+    """More than ten thousand tokens of zero keys and values in one warp's share, then blocks with values: the sum of
+    the zeros' weights stays finite, and the few values are not lost."""
+    rng = np.random.default_rng(64)
+    B, heads, D, block, pages = 64, 8, 256, 128, 128
+    (kc, ks), (vc, vs) = _cache(rng, 10, heads, block, D, 8), _cache(rng, 10, heads, block, D, 8)
+    ks[0], vs[0] = 0.0, 0.0
+    table = np.zeros((B, pages), np.int64)
+    table[:, -2:] = rng.integers(1, 10, (B, 2))
+    total = pages * block - rng.integers(0, 100, B)
+    q = _values(rng.standard_normal((B, heads, D)), bf16)
+    got = _np(H.hbl_kv_attention(_as(q, bf16), _i32(range(B + 1)), _i32(total), _i32(table), *(_dev(a) for a in (kc, ks, vc, vs))))
+    k, v = ref.values(kc, ks, 8), ref.values(vc, vs, 8)
+    for b in (0, 1, 17, 40, 63):
+        want, *sizes = ref.attention(q[b:b + 1], [0, 1], total[b:b + 1], table[b:b + 1], k, v, D ** -0.5, vs)
+        assert np.all(np.abs(got[b] - want[0]) <= ref.attention_tolerance(want, *sizes, pages * block, not bf16, not bf16)[0])
+
+
+@pytest.mark.parametrize("new", [1, 90])
+@pytest.mark.parametrize("bf16", [True, False])
+def test_attention_of_zeros_beside_large_values(H, new, bf16):
+    """Blocks of zeros keep their share of the sum beside values of 2^48, and values of 2^-40 are not zeros."""
+    def mend(table, kc, ks, vc, vs, q):
+        vs[table[0, :5]] = 0.0
+        vs[table[0, 5:]] *= np.float32(2.0 ** 48)
+        vs[table[1]] *= np.float32(2.0 ** -40)
+    _attend(H, np.random.default_rng(65 + new), [new, new], np.array([150, 130]), 8, 2, 64, 16, 8, bf16, mend=mend)
+
+
 @pytest.mark.parametrize("new", [1, 70])
 def test_attention_of_uneven_scales(H, new):
     """Blocks of zero, tiny and large gamma, and scores far apart (a key that takes nearly all the weight while its
