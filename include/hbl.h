@@ -349,8 +349,14 @@ hbl_status hbl_kv_quant(const void* x, hbl_dtype xt, int64_t rows, int64_t D, in
  *   table        device, [B][width], updated in place: entries of blocks that
  *                a request did not have yet are written, no others; blocks
  *                past `width` are not given out
- *   T            rows of the step's token batch (it may be longer than the
- *                sum of `added`), 1 .. 2^26
+ *   T            rows of the step's token batch, 1 .. 2^26: the sum of `added`
+ *                or more.  With fewer the plan is not one to go on with: total,
+ *                table and taken_out are those of all of `added`, while
+ *                row_start, slots and positions end at T, so that the calls
+ *                below would place the rows of the request that T cuts at its
+ *                end, over tokens that nobody wrote.  It shows in the outputs:
+ *                the sum of total - cached is above row_start[B] then, and
+ *                equal to it otherwise
  *   total        device, [B] (output): cached + added
  *   row_start    device, [B + 1] (output): first token row of each request,
  *                and the end of the last (no entry above T)

@@ -535,7 +535,8 @@ def hbl_kv_plan(cached, added, free_blocks, taken, table, block: int, T: int, to
                 positions=None, taken_out=None, stream=None):
     """One serving step's bookkeeping from int32 lengths cached, added [B]: writes the new entries of table
     [B][width] (blocks from free_blocks, from place taken[0] on) and returns (total [B], row_start [B + 1],
-    slots [T], positions [T], taken_out [1])."""
+    slots [T], positions [T], taken_out [1]).  T, the rows of the batch, is at least the sum of added: a plan that cuts
+    a request (total - cached sums to more than row_start[B]) is not for hbl_kv_append and hbl_kv_attention."""
     torch = _torch()
     dev, i32 = _here(table), torch.int32
     B, width = table.shape

@@ -100,6 +100,18 @@ def test_plan_by_hand():
     assert pos.tolist() == [3, 4, 0, 1, 2, 3, 4, 0, -1]
 
 
+def test_a_plan_that_cuts_a_request_shows():
+    """T at or above the sum of `added`: the sum of total - cached is row_start[B], and positions are what the attention
+    takes them to be, total - n + i.  Below it the sums differ, which is how a caller sees that rows were cut."""
+    cached, added, free = [3, 10, 0], [2, 5, 4], list(range(20, 40))
+    for T in (11, 14, 9, 6, 1):
+        _, total, rows, _, pos, _ = ref.plan(cached, added, free, 0, np.full((3, 8), -1), 4, T)
+        whole = (total - cached).sum() == rows[-1]
+        assert whole == (T >= 11)
+        as_attended = [total[b] - (rows[b + 1] - rows[b]) + i for b in range(3) for i in range(rows[b + 1] - rows[b])]
+        assert (as_attended == pos[:rows[-1]].tolist()) == whole
+
+
 @pytest.mark.parametrize("bits", [2, 3, 8])
 def test_cache_values_are_within_half_a_step(bits):
     """A value is held to half a step of its block's gamma, gamma / L, and a requantized one to half a step more for
