@@ -379,9 +379,12 @@ hbl_status hbl_kv_plan(const int32_t* cached, const int32_t* added, int64_t B, i
  *             k + t * k_stride elements (columns of a wider matrix are fine:
  *             strides are multiples of 16 bytes)
  *   slots     device, [T]: where each row goes; rows with a slot below 0 or
- *             past the cache are passed over.  Rows of one block stand
- *             together in rising order, as hbl_kv_plan lays them out, and no
- *             slot occurs twice
+ *             past the cache are passed over.  Rows of one block are
+ *             neighbours with consecutive slots, as hbl_kv_plan lays them
+ *             out: one run a block and call, with no gap and no row that is
+ *             passed over inside it, and no slot twice.  (Two runs in one block
+ *             are written at once, under one scale: what the block holds then
+ *             is undefined; write them with two calls.)
  * Per (block, head) that gets rows, with m their max|x|: a block whose first
  * token is among them starts with gamma = m; in a block that holds earlier
  * tokens gamma' = max(gamma, m), and where that is larger their codes are

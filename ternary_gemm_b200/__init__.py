@@ -559,7 +559,8 @@ def hbl_kv_plan(cached, added, free_blocks, taken, table, block: int, T: int, to
 
 def hbl_kv_append(k, v, slots, k_codes, k_scales, v_codes, v_scales, bits: int = 8, stream=None):
     """Writes rows k, v [T][H][D] (float32/bf16; columns of a wider matrix are fine) into the cache at int32 slots [T]:
-    codes uint8 [blocks][H][block][D], scales float32 [blocks][H], both in place.  Returns the four."""
+    codes uint8 [blocks][H][block][D], scales float32 [blocks][H], both in place.  Returns the four.  Rows of one block
+    are neighbours with consecutive slots (hbl_kv_plan's are); rows with a slot outside the cache are passed over."""
     dev = _here(k_codes)
     n, H, block, D = _cache_shape(dev, k_codes, k_scales, v_codes, v_scales)
     ks, vs = _head_rows("k", k, dev), _head_rows("v", v, dev)

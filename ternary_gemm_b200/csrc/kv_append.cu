@@ -6,8 +6,9 @@
 //
 // and earlier codes of the block requantized from (float)(2 q - L) *
 // fl(gamma / L) where gamma grew.  The rows of one block stand together in the
-// batch, so the first of them (the leader: its predecessor's slot is not the
-// one before, or its own starts a block) finds the run by reading slots alone.
+// batch at consecutive slots, so the first of them (the leader: its
+// predecessor's slot is not the one before, or its own starts a block) finds the
+// run by reading slots alone.
 //
 // A CTA takes a group of rows, some heads, and K or V, and works on the runs
 // that begin in its group: long runs with all its threads, short ones (a

@@ -112,6 +112,28 @@ def test_a_plan_that_cuts_a_request_shows():
         assert (as_attended == pos[:rows[-1]].tolist()) == whole
 
 
+def test_plan_lays_the_rows_of_a_block_out_as_one_run():
+    """What the write asks of its slots: each block's rows are neighbours, at consecutive slots, with nothing between."""
+    rng = np.random.default_rng(8)
+    for block in (16, 64):
+        cached, added = rng.integers(0, 100, 30), rng.integers(0, 150, 30)
+        _, _, _, slots, _, _ = ref.plan(cached, added, rng.permutation(900)[:300], 0, _owned(rng, cached, block, 17), block, int(added.sum()) + 9)
+        rows = np.flatnonzero(slots >= 0)
+        for page in set((slots[rows] // block).tolist()):
+            own = rows[slots[rows] // block == page]
+            assert (np.diff(own) == 1).all() and (np.diff(slots[own]) == 1).all()
+
+
+def _owned(rng, cached, block, width):
+    """A table whose requests own blocks that no free list names."""
+    table, at = np.full((len(cached), width), -1), 1000
+    for b, c in enumerate(cached):
+        n = min(-(-int(c) // block), width)
+        table[b, :n] = np.arange(at, at + n)
+        at += n
+    return table
+
+
 @pytest.mark.parametrize("bits", [2, 3, 8])
 def test_cache_values_are_within_half_a_step(bits):
     """A value is held to half a step of its block's gamma, gamma / L, and a requantized one to half a step more for
