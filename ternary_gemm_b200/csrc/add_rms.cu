@@ -302,6 +302,10 @@ add_rms_grad_kernel(const void* __restrict__ h, int64_t M, int K, const float* _
   const int rl = threadIdx.x / T, t = threadIdx.x % T;
   const int vectors = K / 8;
   const float inv_k = __fdiv_rn(1.0f, (float)K);
+  // Row sums are taken of h 2^-8: h^2 over at most 2^15 columns stays in float wherever its mean does, which is where
+  // the forward's rstd is not 0.  Powers of two: the same bits.
+  constexpr float kDown = 0x1p-8f;
+  const float mean_h2 = inv_k * 0x1p16f, mean_gh = inv_k * 0x1p8f;
   const int64_t grid = gridDim.x, step = grid * S::R;
   const uint32_t ring = sm100::smem_u32(ring_bytes);
   float acc[E][8], w[kGain ? E : 1][8];
@@ -367,8 +371,9 @@ add_rms_grad_kernel(const void* __restrict__ h, int64_t M, int K, const float* _
       if constexpr (!kGain) load_gain<S>(gain, j, vectors, w[0]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        s = fmaf(hv[e], hv[e], s);
-        d = fmaf(gv[e] * w[kGain ? j : 0][e], hv[e], d);
+        const float v = hv[e] * kDown;
+        s = fmaf(v, v, s);
+        d = fmaf(gv[e] * w[kGain ? j : 0][e], v, d);
       }
       ss += s;
       dot += d;
@@ -389,8 +394,8 @@ add_rms_grad_kernel(const void* __restrict__ h, int64_t M, int K, const float* _
         dot += r.y;
       }
     }
-    const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(fmaf(ss, inv_k, 1e-5f)));
-    const float c = dot * rstd * inv_k;
+    const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(fmaf(ss, mean_h2, 1e-5f)));
+    const float c = dot * rstd * mean_gh;
 #pragma unroll
     for (int j = 0; j < E; ++j) {
       const int i = j * T + t;

@@ -785,6 +785,24 @@ def test_add_rms_backward_in_place_and_alone(H):
     assert torch.equal(alone, want_gain)
 
 
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("M,K,size", [(9, 4096, 2e18), (700, 2560, 2e18), (5, 32768, 2e18), (9, 1040, 1e-30)])
+def test_add_rms_backward_of_large_and_small_rows(H, M, K, size, bf16):
+    """Rows whose squares add up past float's range while their mean, and so the forward's rstd, does not; and tiny ones.
+    The forward's codes and the gradient are those of the definition all the same."""
+    rng = np.random.default_rng(K)
+    h, g_t = _values(rng.standard_normal((M, K)) * size, bf16), _values(rng.standard_normal((M, K)), bf16)
+    gain = (1.0 + 0.2 * rng.standard_normal(K)).astype(np.float32)
+    _, _, q, s = ref.add_rms_quant(h, None, gain, 8, bf16)
+    _, got_q, got_s = H.hbl_add_rms_quant(_as(h, bf16), 8, gain=_dev(gain))
+    assert np.array_equal(to_host(got_q), q) and np.array_equal(to_host(got_s), s)
+    wx, wg, terms = ref.add_rms_backward(h, gain, g_t, None)
+    g_x, g_gain = H.hbl_add_rms_quant_backward(_as(h, bf16), _as(g_t, bf16), gain=_dev(gain))
+    assert np.all(np.abs(_np(g_x) - wx) <= _grad_tolerance(terms, K, M, wx, bf16))
+    n = np.abs(h / np.sqrt((h.astype(np.float64) ** 2).mean(1, keepdims=True) + 1e-5) * g_t).sum(0)
+    assert np.all(np.abs(_np(g_gain) - wg) <= (K / 256 + M / 128 + 350) * 2.0 ** -24 * n)
+
+
 def test_add_rms_backward_against_differences(H):
     """g_x of the kernel (float) against central differences of the 64-bit value."""
     rng = np.random.default_rng(5)
