@@ -461,7 +461,8 @@ size_t hbl_add_rms_quant_backward_workspace_bytes(int64_t M, int64_t K);
  *   gain   device, K floats, or NULL for 1
  *   g_x    device, [M][K] of dtype xt (output; may be g_h itself)
  *   g_gain device, K floats (output), or NULL where it is not wanted
- * Sums over a row are float, those over the rows float in fixed order.
+ * Sums over a row are float; the gain's over the rows are float over the rows
+ * that one CTA takes, then double, in fixed order.
  * workspace device, 256-byte aligned, >= the query's bytes; scratch, of one
  * call at a time. */
 hbl_status hbl_add_rms_quant_backward(const void* h, hbl_dtype xt, int64_t M, int64_t K, const float* gain,

@@ -17,7 +17,8 @@
 //
 // The gain's gradient is summed over the rows in registers by a grid that
 // stays (a CTA's rows one after the other), then over the CTAs by a second
-// kernel in fixed order.
+// kernel, in double and in fixed order (in float: 0.1 to 0.3 us less, and errors
+// of 1.06e-7 of the norm instead of 0.77e-7 at 1001 float rows).
 //
 // Measured at 8192 bf16 rows of 4096: forward 42 us, 5.6 TB/s, 85% of a plain
 // copy's rate; gradient 49 us, 5.5 TB/s, 83% (about 45 of them the rows, the
@@ -459,18 +460,19 @@ add_rms_grad_kernel(const void* __restrict__ h, int64_t M, int K, const float* _
   }
 }
 
-// g_gain[k] = sum of the partial sums [count][K]: 32 columns per CTA, 32 warps
-// on every 32nd row (the partial sums are in L2: round trips are what counts)
+// g_gain[k] = sum of the partial sums [count][K], in double: 32 columns per CTA,
+// 32 warps on every 32nd row (the partial sums are in L2: round trips are what
+// counts)
 constexpr int kSumWarps = 32;
 __global__ void __launch_bounds__(kSumWarps * 32)
 gain_sum_kernel(const float* sums, int count, int K, float* g_gain) {
-  __shared__ float part[kSumWarps][33];
+  __shared__ double part[kSumWarps][33];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = blockIdx.x * 32 + lane;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  float s = 0.0f;
+  double s = 0.0;
   if (k < K) {
 #pragma unroll 8
-    for (int i = warp; i < count; i += kSumWarps) s += sums[(int64_t)i * K + k];
+    for (int i = warp; i < count; i += kSumWarps) s += (double)sums[(int64_t)i * K + k];
   }
   part[warp][lane] = s;
   __syncthreads();
@@ -478,7 +480,7 @@ gain_sum_kernel(const float* sums, int count, int K, float* g_gain) {
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   const int to = blockIdx.x * 32 + warp;
-  if (lane == 0 && to < K) g_gain[to] = s;
+  if (lane == 0 && to < K) g_gain[to] = (float)s;
 }
 
 // f(Rows<T, E>()) for the rows of K values

@@ -770,6 +770,23 @@ def test_add_rms_backward_of_many_rows(H, M, K, bf16, gt_bf16):
     assert got is g_h and torch.equal(got, g_x)
 
 
+def test_add_rms_backward_gain_over_ctas(H):
+    """The partial sums of CTAs are added in double: large ones of either sign that cancel leave the small ones whole.
+    With h of +-1 the normalised values of all rows are equal in size, so +-2^30 cancel exactly; what remains is off by
+    the roundings of rstd (three operations), of a product and of the result, each half a step."""
+    import torch
+    M, K = 128, 1024                                            # at most a row a CTA
+    rng = np.random.default_rng(66)
+    h = np.sign(rng.standard_normal((M, K))).astype(np.float32)
+    h[96] = h[0]
+    g_t = rng.uniform(0.5, 1.5, (M, K)).astype(np.float32)
+    g_t[0], g_t[96] = 2.0 ** 30, -2.0 ** 30
+    _, got = H.hbl_add_rms_quant_backward(_dev(h), _dev(g_t), g_gain=torch.empty(K, device="cuda"))
+    small = np.delete(h.astype(np.float64) * g_t, (0, 96), 0) / np.sqrt(1.0 + 1e-5)
+    tol = 5 * 2.0 ** -24 * np.abs(small).sum(0) + 2.0 ** -52 * 2.0 ** 31 * 8     # and a few double additions of 2^30
+    assert np.all(np.abs(_np(got) - small.sum(0)) <= tol)
+
+
 def test_add_rms_backward_in_place_and_alone(H):
     """g_x over g_h; without a gain no gain gradient; a gain gradient without a gain is the sum all the same."""
     import torch
