@@ -706,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, NT, F32)) kv_attent
         // The tensor cores' sums drop what lies below the accumulator's last bit, always toward zero: over the hundreds
         // of products of a long item that would show in float outputs (1.5e-6 of them at 2448 tokens).  A tile's
         // products of float queries begin at 0, and an ordinary addition takes them to the row's.
-        float of_tile[2][F32 ? NT : 1][4] = {};
+        [[maybe_unused]] float of_tile[2][F32 ? NT : 1][4] = {};
         unrolled<2>([&](auto half) {
           uint32_t w[4];
           ldmatrix4t<half * 2 * kHalf + (x >> 3) * 128>(at, w);
@@ -949,6 +949,11 @@ template <int D>
 cudaError_t launch_d(const KvAttentionArgs& a, cudaStream_t stream) {
   // Rows of one request and cached head, on average: up to eight share one
   // pass over the codes in half the products that sixteen need.
+  // At D = 256 sixteen bf16 rows spill a little (300 bytes) and are kept for
+  // prompts, the only path that those have: two chunks of 512 rows over 4096
+  // tokens, 16 heads over 4, take 374 us so and 413 with eight; 32 x 4 draft
+  // rows, 32 heads over 8, 135 and 133, 64 single rows, 32 heads over 2, 111
+  // and 108.
   const bool few = a.T * (a.Hq / a.Hkv) <= (int64_t)8 * a.B;
   if (a.q_bf16) return few ? launch<D, 1, false>(a, stream) : launch<D, 2, false>(a, stream);
   if constexpr (D == 256) return launch<D, 1, true>(a, stream);  // sixteen float rows would not fit the registers
