@@ -419,7 +419,10 @@ size_t hbl_kv_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t Hkv, int6
  * most 2^31 - 256.  Scores, softmax sums and outputs are
  * accumulated in float; codes enter the products exactly; queries (scaled by a
  * power of two per row) and weights enter them as fp16, in two parts when q is
- * HBL_F32, so its products carry 22 bits.  A block of values with gamma / L
+ * HBL_F32, so its products carry 22 bits.  A value enters as (2 (q - z) + 1) u
+ * with u = gamma / L, z = 2^(bits - 1): the 1 is weighed by the unrounded
+ * weights, so that their rounding costs an output at most 2^-11 (2^-22)
+ * sum_j p_j (|v_j| + u_j).  A block of values with gamma / L
  * below 2^-100 counts as all zeros; blocks keep their precision side by side where
  * gamma / L differs by less than a factor of 2^100. */
 hbl_status hbl_kv_attention(const void* q, hbl_dtype qt, int64_t T, int64_t q_stride, int64_t Hq, int64_t Hkv,
