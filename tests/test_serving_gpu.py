@@ -1035,6 +1035,41 @@ def test_memory_of_a_call_on_another_stream_is_its_own(H):
         assert all(bool((m == 7).all()) for m in mine)
 
 
+def test_calls_on_a_forked_stream_of_a_capture(H):
+    """stream= with buffers of the calls' own, on a stream that a captured one forked off and joins again."""
+    import torch
+    rng = np.random.default_rng(67)
+    total, table = rng.integers(1, 900, 6), rng.permutation(180).reshape(6, 30)
+    cache = [_dev(a) for a in _cache(rng, 180, 2, 32, 64, 8) + _cache(rng, 180, 2, 32, 64, 8)]
+    q, x = _as(rng.standard_normal((8, 8, 64)), True), _as(rng.standard_normal((70, 1040)), True)
+    args = (_i32(range(7)), _i32(total), _i32(table), *cache)
+    gain = torch.ones(1040, device="cuda")
+
+    def step(stream):
+        o = H.hbl_kv_attention(q, *args, stream=stream)
+        h, codes, scales = H.hbl_add_rms_quant(x, 8, gain=gain, stream=stream)
+        return (o, h, codes, scales) + H.hbl_add_rms_quant_backward(h, x, gain=gain, stream=stream)
+
+    main, fork = torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.stream(main):
+        step(None)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        fork.wait_stream(main)
+        outs = step(fork)
+        main.wait_stream(fork)
+    for _ in range(3):
+        q.copy_(_as(rng.standard_normal((8, 8, 64)), True))
+        x.copy_(_as(rng.standard_normal((70, 1040)), True))
+        want = step(None)
+        for t in outs:
+            t.view(torch.uint8).fill_(0x55)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
 def test_the_binding_refuses(H):
     """Wrong types, shapes, strides, devices: nothing is launched on tensors that do not fit."""
     import torch
