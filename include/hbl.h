@@ -404,7 +404,8 @@ size_t hbl_kv_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t Hkv, int6
  * stands at position p = total[b] - n + i and sees tokens 0 .. p:
  *   o = sum_j softmax_j(scale q . k_j) v_j,   query head h reads head h / (Hq / Hkv)
  * One row per request is a decode step; many rows are a prompt or a chunk of
- * one; both may stand in one batch.  A row that sees no token gives 0, rows
+ * one; both may stand in one batch (which is worked on as its average asks: a
+ * long prompt and many single rows take less time in two calls).  A row that sees no token gives 0, rows
  * outside [row_start[0], row_start[B]) of o are left as they were, and tokens
  * past the table or in a block outside the cache are not seen.
  *   q          device, T rows of Hq heads of D values of dtype qt, row t at

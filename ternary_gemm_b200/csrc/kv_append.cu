@@ -18,8 +18,11 @@
 // CTAs an SM to hide it, six prompts took 70 us instead of 64).  Bytes are all
 // there is to it: 2 (4) in and 1 out per value; for few rows, the launch and
 // four dependent reads.  Measured: six prompts of up to 2731 rows (32 heads of
-// 128, 350 MB in and out) 64 us, 5.5 TB/s, 84% of a plain copy's rate; 64
-// single rows 4 us each call in a graph.
+// 128, 350 MB in and out) 64 us, 5.5 TB/s, 84% of a plain copy's rate (float
+// rows 153 us, 58%; 8 heads of 256 in blocks of 128, whose rows past a thread's
+// registers are read twice, 50%); 64 single rows 4 us each call in a graph; 2048
+// single rows into blocks of 64 that all grow, codes read and written again,
+// 162 us, 3.3 TB/s.
 #include <cstdint>
 
 #include "common.cuh"

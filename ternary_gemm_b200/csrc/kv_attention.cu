@@ -11,7 +11,9 @@
 // The value blocks' scale is part of the weight, so the running maximum is
 // that of s_j + ln u_v(j): the weights that enter the second product lie in
 // [0, 2^15] with the largest near the top, where fp16 keeps 11 bits of
-// everything down to 2^-29 of it.  Queries are scaled by a power of two per
+// everything down to 2^-29 of it.  Their rounding falls on 2 v'_j; the 1 beside
+// it and the sum below take them as they were.  What blocks of zeros do to the
+// sum is said at kLeastValueScale.  Queries are scaled by a power of two per
 // row into fp16 (bf16 values exactly; float ones as two fp16 parts, 22 bits,
 // and the weights too).
 //
@@ -28,9 +30,10 @@
 // kernel joins them in order.
 //
 // Measured (codes' bytes over the call's time): 64 requests of up to 8192
-// tokens, 32 heads over 8 of 128: 108 us, 5.3 TB/s, 81% of a plain copy's rate;
-// two of up to 131072: 78 us, 5.4 TB/s, 83%.  The main kernel alone moves its
-// bytes at 5.85 TB/s; what is left is the join (4 us), the first loads of
+// tokens, 32 heads over 8 of 128: 109 us, 5.3 TB/s, 80% of a plain copy's rate;
+// two of up to 131072: 79 us, 5.4 TB/s, 82%.  (Heads of 64: 70%, of 256: 69%, of
+// 32: 50%; float queries at 128: 76%; four rows a request: 54%, float 41%.)  The
+// main kernel alone moves its bytes at 5.7 TB/s; what is left is the join (4 us), the first loads of
 // every warp, and shares that end unevenly.  One request of 777 tokens takes 12 us
 // on the device: two launches and a chain of six dependent reads (lengths,
 // table, scales, codes, part, parts of others).
@@ -63,7 +66,8 @@ constexpr int kMinTiles = 2;
 // and warps enough to hide the products' latency, at the registers that the
 // accumulators (4 NT D / 16 per thread) and the queries leave.  At D = 128 two
 // blocks with two tiles ahead took 77 us where three with one ahead took 80
-// (two requests of 131072 tokens), and 23 against 25 (one of 32768).
+// (two requests of 131072 tokens), and 23 against 25 (one of 32768).  Past some
+// 2100 requests their prefix sums leave room for one of the two.
 __host__ __device__ constexpr int blocks_per_sm(int D, int NT, bool f32) {
   const int weight = D * NT * (f32 ? 3 : 2);   // registers go with accumulators and query parts
   return D == 256 ? 1 : (D == 128 ? 2 : (weight <= 128 ? 4 : 3));

@@ -12,7 +12,8 @@
 // weights of half a tile add up to more than 2^15: no weight can pass fp16's
 // range, no maximum is taken of a tile, and the accumulator in tensor memory is
 // seldom rescaled.  fp16 keeps 11 bits of all weights down to 2^-21 of the
-// reference's at the least.  (A reference that followed after four powers of
+// reference's at the least; the 1 beside 2 v' and the sum below take them
+// unrounded.  (A reference that followed after four powers of
 // two, which some warp of a CTA met in every other tile: 571 us at three
 // requests of up to 2048 rows over 8192 tokens; after eight, with a maximum of
 // every tile: 406; without: 379, and 367 with the start and end of a CTA
@@ -30,8 +31,8 @@
 //                   O += W V with W from tensor memory (it lies where S was),
 //                   the two row tiles in turn, so that one tile's softmax runs
 //                   under the other's products
-// Measured there: 370 us, 860 TFLOP/s of the causal products, 52% of the
-// rate of a long library product; 4000 clocks for 256 rows over 128 tokens, of
+// Measured there: 369 us, 860 TFLOP/s of the causal products, 52% of the
+// rate of a long library product (heads of 64: 319 us, 500 TFLOP/s, 30%); 4000 clocks for 256 rows over 128 tokens, of
 // which the products take 2050 and a row tile's softmax 2700 (the exponentials
 // of both 2050, at their unit's rate).  What bounds it is the chain of a row
 // tile: its next scores go where its weights lie, so they are begun only when
@@ -877,7 +878,9 @@ cudaError_t launch(const KvAttentionArgs& a, cudaStream_t stream) {
 // tokens: about 25 rows a head and request, P = 15, 181 us here against 152 in
 // kv_attention.cu; 50 rows, P = 28, 192 against 277.  One request of 16384,
 // shared: 64 rows, P = 36, 48 us against 41; 128 rows, P = 72, 48 against 62;
-// 1024 rows, 95 against 347.
+// 1024 rows, 95 against 347.  The average is all the host knows: one prompt of
+// 2048 rows over 4096 tokens beside 63 single rows comes here whole, 417 us,
+// where two calls take 111 and 123.
 constexpr int64_t kWorkAlone = 18, kWorkShared = 45;
 bool kv_attention_prompt_supports(const KvAttentionArgs& a) {
   if (!a.q_bf16 || (a.D != 64 && a.D != 128)) return false;
