@@ -31,7 +31,7 @@
 //
 // Measured (codes' bytes over the call's time): 64 requests of up to 8192
 // tokens, 32 heads over 8 of 128: 109 us, 5.3 TB/s, 80% of a plain copy's rate;
-// two of up to 131072: 79 us, 5.4 TB/s, 82%.  (Heads of 64: 70%, of 256: 69%, of
+// two of up to 131072: 78 us, 5.4 TB/s, 83%.  (Heads of 64: 70%, of 256: 69%, of
 // 32: 50%; float queries at 128: 76%; four rows a request: 54%, float 41%.)  The
 // main kernel alone moves its bytes at 5.7 TB/s; what is left is the join (4 us), the first loads of
 // every warp, and shares that end unevenly.  One request of 777 tokens takes 12 us
@@ -628,8 +628,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, NT, F32)) kv_attent
         kind[half] = __shfl_sync(0xffffffffu, kind_now, from);
         ku[half] = __shfl_sync(0xffffffffu, ku_now, from);
         lu[half] = __shfl_sync(0xffffffffu, lu_now, from);
-        lift[half] = kind[half] == 1 ? kSumLog - kLeastValueLog : 0.0f;
-        inv_vu[half] = kind[half] == 1 ? 1.0f : ex2(-lu[half]) * kSumScale;
+        lift[half] = kind[half] == 1 ? -kLeastValueLog : 0.0f;
+        inv_vu[half] = kind[half] == 1 ? 1.0f : ex2(-lu[half]);
       }
       const int tok0 = (first + 2 * i) * kTok;
       const bool masked = kind[0] == 2 || kind[1] == 2 || tok0 + kStep > all_see;
@@ -664,9 +664,9 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, NT, F32)) kv_attent
               m[nt][x], row_max(fmaxf(fmaxf(p[0][0][x], p[0][1][x]), fmaxf(p[1][0][x], p[1][1][x]))));
           // a row that has seen nothing keeps -inf, with 0 in its place in the differences
           const float base = top == -INFINITY ? 0.0f : top, off = kTop - base;
-          const Shrink by = shrink(m[nt][x] - base);
-          grow[nt][x] = by.near;
-          l[nt][x] *= by.far;
+          const float rise = m[nt][x] - base;  // shrink(), its second factor where there is one
+          grow[nt][x] = ex2(fmaxf(rise, -100.0f));
+          if (rise < -100.0f) l[nt][x] *= ex2(rise + 100.0f);
           grows |= grow[nt][x] != 1.0f;
           m[nt][x] = top;
 #pragma unroll
@@ -691,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, NT, F32)) kv_attent
         for (int x = 0; x < 2; ++x) {
           const float s0 = p[0][0][x] + p[0][1][x], s1 = p[1][0][x] + p[1][1][x];
           w_sum[nt][x] = fmaf(w_sum[nt][x], grow[nt][x], (kind[0] == 1 ? 0.0f : s0) + (kind[1] == 1 ? 0.0f : s1));
-          l[nt][x] = fmaf(l[nt][x], grow[nt][x], fmaf(s0, inv_vu[0], s1 * inv_vu[1]));
+          l[nt][x] = fmaf(l[nt][x], grow[nt][x], kSumScale * fmaf(s0, inv_vu[0], s1 * inv_vu[1]));
         }
       }
       if (__any_sync(0xffffffffu, grows)) {

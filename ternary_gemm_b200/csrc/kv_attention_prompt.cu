@@ -478,7 +478,7 @@ kv_attention_prompt_kernel(const KvAttentionArgs a, const int splits, int* err) 
 #pragma unroll 1
           for (int grp = 0; grp < 4; ++grp) {
             const Page p = page_at(pages, 4 * half + grp, q_scale, q_sum);
-            const float c = p.some() ? p.c : p.c + (kLeastValueLog - kSumLog);
+            const float c = p.some() ? p.c : p.c + kLeastValueLog;
             uint32_t s[16];
             tmem_ld16(from + 16 * grp, s);
             landed(s);
@@ -528,7 +528,7 @@ kv_attention_prompt_kernel(const KvAttentionArgs a, const int splits, int* err) 
           }
           run();
         }
-        l += sum;
+        l = fmaf(sum, kSumScale, l);
         ws += all;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
@@ -683,10 +683,9 @@ kv_attention_prompt_kernel(const KvAttentionArgs a, const int splits, int* err) 
         const bool there = (lane == 0 ? id[0] : id[1]) >= 0;
         const float vu = __fdiv_rn(vs, (float)L);
         const bool some = vu >= kLeastValueScale;
-        const float lu = some ? __log2f(vu) : kSumLog;
+        const float lu = some ? __log2f(vu) : 0.0f;
         meta[(i % kMeta) * 8 + cw * 2 + lane] =
-            there ? make_float4(__fdiv_rn(ks, (float)L), lu, some ? ex2(-lu) * kSumScale : 1.0f,
-                                some ? 1.0f : kLeastValueScale / kSumScale)
+            there ? make_float4(__fdiv_rn(ks, (float)L), lu, ex2(-lu), some ? 1.0f : kLeastValueScale)
                   : make_float4(0.0f, -INFINITY, 0.0f, 0.0f);
       }
       convert(k_at + st * S::kTile, id, kv);

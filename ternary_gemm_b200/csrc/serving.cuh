@@ -17,13 +17,13 @@ constexpr int kMaxRequests = 4096;  // the plan and the attention scan them in s
 // first of these (2 to the second) counts as all zeros.  Its weights enter no
 // product: where the running maximum (or reference) is taken they stand as if u
 // were that, below every block with values, and in the sum they are held without
-// u.  The sum is held times 2^-32.  A term of it is then at most 2^(15 + 100 -
-// 32), so fewer than 2^31 tokens stay below 2^114 in float, and beside values of
-// u up to 2^80 a token's part is kept down to 2^-24 of the whole.  (Codes of so
-// small a gamma hold nothing: with the rule's 1e-5 beside it x r vanishes next
+// u.  A term of the sum is then at most 2^(15 + 100); the sum is kept times
+// 2^-20, so that fewer than 2^31 tokens stay below 2^126 in float, and the
+// largest float values (u = 2^120) leave terms of 2^(15 - 120 - 20).  (Codes of
+// so small a gamma hold nothing: with the rule's 1e-5 beside it x r vanishes next
 // to L / 2 from gamma = 2^-42 down, and all codes are one.)
 constexpr float kLeastValueScale = 0x1p-100f, kLeastValueLog = -100.0f;
-constexpr float kSumScale = 0x1p-32f, kSumLog = -32.0f;
+constexpr float kSumScale = 0x1p-20f;
 
 // 2^d for d <= 0 in two factors, the second 1 down to 2^-100.  A sum that zeros
 // have made large takes both, and keeps what 2^d alone would lose below float's

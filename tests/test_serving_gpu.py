@@ -463,6 +463,16 @@ def test_attention_of_zeros_beside_large_values(H, new, bf16):
     _attend(H, np.random.default_rng(65 + new), [new, new], np.array([150, 130]), 8, 2, 64, 16, 8, bf16, mend=mend)
 
 
+@pytest.mark.parametrize("new", [1, 90])
+@pytest.mark.parametrize("bf16", [True, False])
+def test_attention_of_the_largest_values(H, new, bf16):
+    """Values up to 2^118, alone and beside blocks of zeros."""
+    def mend(table, kc, ks, vc, vs, q):
+        vs *= np.float32(2.0 ** 115)
+        vs[table[0, ::2]] = 0.0
+    _attend(H, np.random.default_rng(68 + new), [new, new], np.array([150, 130]), 8, 2, 64, 16, 8, bf16, mend=mend)
+
+
 @pytest.mark.parametrize("new", [1, 70])
 def test_attention_of_uneven_scales(H, new):
     """Blocks of zero, tiny and large gamma, and scores far apart (a key that takes nearly all the weight while its
